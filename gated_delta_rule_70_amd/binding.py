@@ -29,6 +29,11 @@ EXPORTS = ("gdr_chunk_fwd", "gdr_chunk_fwd_bidir", "gdr_chunk_fwd_gated", "gdr_d
            "gdr_gdn2_decode_step",
            "gdr_delta_product_fwd",
            "gdr_chunk_bwd", "gdr_chunk_bwd_workspace_bytes",
+           "gdr_channel_scan_fwd", "gdr_channel_scan_fwd_workspace_bytes", "gdr_channel_scan_states_elems",
+           "gdr_channel_scan_bwd", "gdr_channel_scan_bwd_workspace_bytes", "gdr_channel_scan_step",
+           "gdr_gated_ffn_fwd", "gdr_gated_ffn_bwd", "gdr_gated_ffn_bwd_workspace_bytes",
+           "gdr_linear_ce_fwd", "gdr_linear_ce_fwd_workspace_bytes", "gdr_linear_ce_bwd",
+           "gdr_linear_ce_bwd_workspace_bytes",
            "gdr_status_string", "gdr_last_error", "gdr_abi_version", "gdr_selftest_mfma")
 
 
@@ -43,6 +48,21 @@ class ChunkDims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("Hk", ctypes.c_int64),
                 ("Hv", ctypes.c_int64), ("dk", ctypes.c_int64), ("dv", ctypes.c_int64),
                 ("num_seqs", ctypes.c_int64), ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class ScanDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("num_seqs", ctypes.c_int64), ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class FfnDims(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("D", ctypes.c_int64), ("F", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
+class CeDims(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("D", ctypes.c_int64), ("V", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
 
 
 class DecodeDims(ctypes.Structure):
@@ -84,6 +104,24 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gdr_gdn2_chunk_fwd_workspace_bytes.restype = ctypes.c_int64
     lib.gdr_gdn2_decode_step.argtypes = [p, p, p, p, p, p, p, p, p, ctypes.POINTER(DecodeDims), p]
     lib.gdr_gdn2_decode_step.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    for name, args in (("gdr_channel_scan_fwd", [p] * 11 + [i64, ctypes.POINTER(ScanDims), p]),
+                       ("gdr_channel_scan_bwd", [p] * 16 + [i64, ctypes.POINTER(ScanDims), p]),
+                       ("gdr_channel_scan_step", [p] * 8 + [ctypes.POINTER(ScanDims), p]),
+                       ("gdr_gated_ffn_fwd", [p] * 6 + [ctypes.POINTER(FfnDims), p]),
+                       ("gdr_gated_ffn_bwd", [p] * 10 + [i64, ctypes.POINTER(FfnDims), p]),
+                       ("gdr_linear_ce_fwd", [p] * 6 + [i64, ctypes.POINTER(CeDims), p]),
+                       ("gdr_linear_ce_bwd", [p] * 8 + [i64, ctypes.POINTER(CeDims), p])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = ctypes.c_int
+    for name, args in (("gdr_channel_scan_states_elems", [ctypes.POINTER(ScanDims), i32]),
+                       ("gdr_channel_scan_fwd_workspace_bytes", [ctypes.POINTER(ScanDims), i32]),
+                       ("gdr_channel_scan_bwd_workspace_bytes", [ctypes.POINTER(ScanDims), i32]),
+                       ("gdr_gated_ffn_bwd_workspace_bytes", [ctypes.POINTER(FfnDims)]),
+                       ("gdr_linear_ce_fwd_workspace_bytes", [ctypes.POINTER(CeDims)]),
+                       ("gdr_linear_ce_bwd_workspace_bytes", [ctypes.POINTER(CeDims)])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = i64
     lib.gdr_status_string.argtypes = [ctypes.c_int]
     lib.gdr_status_string.restype = ctypes.c_char_p
     lib.gdr_last_error.argtypes = []
@@ -133,12 +171,12 @@ def _need(t, name, dtype=None, shape=None, device=None):
         raise ValueError("%s must be contiguous" % name)
 
 
-def _dtype_code(dt):
+def _dtype_code(dt, what="q, k, v"):
     if dt == torch.bfloat16:
         return GDR_BF16
     if dt == torch.float32:
         return GDR_F32
-    raise ValueError("q, k, v must be bfloat16 or float32 (got %s)" % dt)
+    raise ValueError("%s must be bfloat16 or float32 (got %s)" % (what, dt))
 
 
 def chunk_fwd(q, k, v, log_alpha, beta, h0=None, cu_seqlens=None, *, chunk: int = 64,
@@ -589,6 +627,211 @@ def gdn2_decode_step(q, k, v, g, b, w, state_in, state_out=None, out=None, *, re
     _check(lib().gdr_gdn2_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(b), _ptr(w), _ptr(state_in),
                                       _ptr(state_out), _ptr(out), ctypes.byref(dims), _stream(q)))
     return out, state_out
+
+
+def _workspace(t, need, dev):
+    """The caller's workspace, or a new one of ``need`` bytes (None where none is needed)."""
+    if need < 0:
+        raise GdrError(2, lib().gdr_last_error().decode())
+    if t is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _need(t, "workspace", torch.uint8, None, dev)
+    return t
+
+
+def _scan_args(x, a, b, A_log, dt_bias, cu_seqlens, reverse):
+    _need(x, "x")
+    dev, dt = x.device, x.dtype
+    code = _dtype_code(dt, "x, a, b")
+    if x.dim() != 3:
+        raise ValueError("x must have shape (B, T, D) (got %s)" % (tuple(x.shape),))
+    B, T, D = x.shape
+    _need(a, "a", dt, (B, T, D), dev)
+    _need(b, "b", dt, (B, T, D), dev)
+    _need(A_log, "A_log", torch.float32, (D,), dev)
+    _need(dt_bias, "dt_bias", torch.float32, (D,), dev)
+    S = B
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
+        S = cu_seqlens.shape[0] - 1
+    return ScanDims(B, T, D, S if cu_seqlens is not None else 0, code, GDR_REVERSE if reverse else 0), S, dev
+
+
+def channel_scan_fwd(x, a, b, A_log, dt_bias, h0=None, cu_seqlens=None, *, reverse: bool = False, out=None,
+                     hT=None, want_state: bool = True, want_states: bool = False, workspace=None):
+    """The gated linear recurrence per channel over whole sequences (``gdr_channel_scan_fwd``).
+
+    x, a, b [B, T, D] (bf16 or fp32, one dtype); A_log, dt_bias [D] fp32; h0 [S, D] fp32 or None;
+    cu_seqlens int32 [S+1] (device) or None. Returns (out [B, T, D], hT [S, D] or None, states or
+    None); ``want_states`` keeps the block states ``channel_scan_bwd`` needs. ``hT`` may be ``h0``."""
+    dims, S, dev = _scan_args(x, a, b, A_log, dt_bias, cu_seqlens, reverse)
+    if h0 is not None:
+        _need(h0, "h0", torch.float32, (S, dims.D), dev)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", x.dtype, x.shape, dev)
+    if hT is not None:
+        _need(hT, "hT", torch.float32, (S, dims.D), dev)
+    elif want_state:
+        hT = torch.empty((S, dims.D), dtype=torch.float32, device=dev)
+    packed = int(cu_seqlens is not None)
+    d = ctypes.byref(dims)
+    states = None
+    if want_states:
+        n = lib().gdr_channel_scan_states_elems(d, packed)
+        if n < 0:
+            raise GdrError(2, lib().gdr_last_error().decode())
+        states = torch.empty(n, dtype=torch.float32, device=dev)
+    ws = _workspace(workspace, lib().gdr_channel_scan_fwd_workspace_bytes(d, packed), dev)
+    _check(lib().gdr_channel_scan_fwd(_ptr(x), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias), _ptr(h0),
+                                      _ptr(cu_seqlens), _ptr(out), _ptr(hT), _ptr(states), _ptr(ws),
+                                      0 if ws is None else ws.numel(), d, _stream(x)))
+    return out, hT, states
+
+
+def channel_scan_bwd(x, a, b, A_log, dt_bias, states, dout, cu_seqlens=None, dhT=None, *, reverse: bool = False,
+                     want_dh0: bool = True, workspace=None):
+    """Gradients of ``channel_scan_fwd`` (``gdr_channel_scan_bwd``): its inputs, the ``states`` it
+    kept, dout [B, T, D] and dhT [S, D] fp32 or None. Returns (dx, da, db [B, T, D] in x's dtype,
+    dA_log, ddt_bias [D] fp32, dh0 [S, D] fp32 or None)."""
+    dims, S, dev = _scan_args(x, a, b, A_log, dt_bias, cu_seqlens, reverse)
+    packed = int(cu_seqlens is not None)
+    d = ctypes.byref(dims)
+    _need(dout, "dout", x.dtype, x.shape, dev)
+    if dhT is not None:
+        _need(dhT, "dhT", torch.float32, (S, dims.D), dev)
+    _need(states, "states", torch.float32, (lib().gdr_channel_scan_states_elems(d, packed),), dev)
+    dx, da, db = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+    dA_log, ddt_bias = torch.empty_like(A_log), torch.empty_like(A_log)
+    dh0 = torch.empty((S, dims.D), dtype=torch.float32, device=dev) if want_dh0 else None
+    ws = _workspace(workspace, lib().gdr_channel_scan_bwd_workspace_bytes(d, packed), dev)
+    _check(lib().gdr_channel_scan_bwd(_ptr(x), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias), _ptr(states),
+                                      _ptr(cu_seqlens), _ptr(dout), _ptr(dhT), _ptr(dx), _ptr(da), _ptr(db),
+                                      _ptr(dA_log), _ptr(ddt_bias), _ptr(dh0), _ptr(ws),
+                                      0 if ws is None else ws.numel(), d, _stream(x)))
+    return dx, da, db, dA_log, ddt_bias, dh0
+
+
+def channel_scan_step(x, a, b, A_log, dt_bias, state_in, state_out=None, out=None):
+    """One token of the channel scan (``gdr_channel_scan_step``): x, a, b [N, D]; state_in [N, D] fp32.
+    ``state_out`` defaults to a new tensor; pass ``state_in`` itself to update in place. Returns
+    (out [N, D], state_out)."""
+    _need(x, "x")
+    dev, dt = x.device, x.dtype
+    code = _dtype_code(dt, "x, a, b")
+    if x.dim() != 2:
+        raise ValueError("x must have shape (N, D) (got %s)" % (tuple(x.shape),))
+    N, D = x.shape
+    _need(a, "a", dt, (N, D), dev)
+    _need(b, "b", dt, (N, D), dev)
+    _need(A_log, "A_log", torch.float32, (D,), dev)
+    _need(dt_bias, "dt_bias", torch.float32, (D,), dev)
+    _need(state_in, "state_in", torch.float32, (N, D), dev)
+    if state_out is None:
+        state_out = torch.empty_like(state_in)
+    else:
+        _need(state_out, "state_out", torch.float32, (N, D), dev)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", dt, (N, D), dev)
+    dims = ScanDims(N, 1, D, 0, code, 0)
+    _check(lib().gdr_channel_scan_step(_ptr(x), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias), _ptr(state_in),
+                                       _ptr(state_out), _ptr(out), ctypes.byref(dims), _stream(x)))
+    return out, state_out
+
+
+ACTS = {"silu": 0, "gelu_tanh": 1}
+
+
+def _ffn_args(x, w_gate, w_up, act):
+    _need(x, "x")
+    dev, dt = x.device, x.dtype
+    code = _dtype_code(dt, "x, w_gate, w_up")
+    if x.dim() < 1 or w_gate.dim() != 2:
+        raise ValueError("x must have shape (..., D) and w_gate (F, D) (got %s, %s)" % (tuple(x.shape), tuple(w_gate.shape)))
+    if act not in ACTS:
+        raise ValueError("act must be one of %s" % ", ".join(sorted(ACTS)))
+    D, F = x.shape[-1], w_gate.shape[0]
+    _need(w_gate, "w_gate", dt, (F, D), dev)
+    _need(w_up, "w_up", dt, (F, D), dev)
+    M = 1
+    for n in x.shape[:-1]:
+        M *= n
+    return FfnDims(M, D, F, code, ACTS[act]), dev
+
+
+def gated_ffn_fwd(x, w_gate, w_up, *, act: str = "silu", out=None, want_saved: bool = False):
+    """Both projections of a gated feed-forward block, the activation and the product
+    (``gdr_gated_ffn_fwd``): h = act(x w_gate^T) * (x w_up^T). x [..., D]; w_gate, w_up [F, D] (bf16
+    or fp32, one dtype). Returns (h [..., F], gate, up); the projections gate and up [..., F] are kept
+    for ``gated_ffn_bwd`` with ``want_saved``, else None."""
+    dims, dev = _ffn_args(x, w_gate, w_up, act)
+    shape = tuple(x.shape[:-1]) + (dims.F,)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=dev)
+    else:
+        _need(out, "out", x.dtype, shape, dev)
+    gate = torch.empty_like(out) if want_saved else None
+    up = torch.empty_like(out) if want_saved else None
+    _check(lib().gdr_gated_ffn_fwd(_ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(out), _ptr(gate), _ptr(up),
+                                   ctypes.byref(dims), _stream(x)))
+    return out, gate, up
+
+
+def gated_ffn_bwd(x, w_gate, w_up, gate, up, dh, *, act: str = "silu", workspace=None):
+    """Gradients of ``gated_ffn_fwd`` (``gdr_gated_ffn_bwd``): its inputs, the gate and up it kept and
+    dh [..., F]. Returns (dx [..., D], dw_gate, dw_up [F, D]) in x's dtype."""
+    dims, dev = _ffn_args(x, w_gate, w_up, act)
+    shape = tuple(x.shape[:-1]) + (dims.F,)
+    for t, n in ((gate, "gate"), (up, "up"), (dh, "dh")):
+        _need(t, n, x.dtype, shape, dev)
+    dx, dwg, dwu = torch.empty_like(x), torch.empty_like(w_gate), torch.empty_like(w_up)
+    ws = _workspace(workspace, lib().gdr_gated_ffn_bwd_workspace_bytes(ctypes.byref(dims)), dev)
+    _check(lib().gdr_gated_ffn_bwd(_ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(gate), _ptr(up), _ptr(dh), _ptr(dx),
+                                   _ptr(dwg), _ptr(dwu), _ptr(ws), 0 if ws is None else ws.numel(),
+                                   ctypes.byref(dims), _stream(x)))
+    return dx, dwg, dwu
+
+
+def _ce_args(x, weight, targets):
+    _need(x, "x")
+    dev, dt = x.device, x.dtype
+    code = _dtype_code(dt, "x, weight")
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError("x must have shape (N, D) and weight (V, D) (got %s, %s)" % (tuple(x.shape), tuple(weight.shape)))
+    N, D = x.shape
+    V = weight.shape[0]
+    _need(weight, "weight", dt, (V, D), dev)
+    _need(targets, "targets", torch.int64, (N,), dev)
+    return CeDims(N, D, V, code, 0), dev
+
+
+def linear_ce_fwd(x, weight, targets, *, workspace=None):
+    """Softmax cross entropy of x weight^T per token, the logits never kept (``gdr_linear_ce_fwd``).
+    x [N, D], weight [V, D] (bf16 or fp32, one dtype); targets [N] int64, a value outside 0 .. V-1 (as
+    -100) for a token that bears no loss. Returns (loss [N], lse [N]) fp32."""
+    dims, dev = _ce_args(x, weight, targets)
+    loss = torch.empty(dims.N, dtype=torch.float32, device=dev)
+    lse = torch.empty_like(loss)
+    ws = _workspace(workspace, lib().gdr_linear_ce_fwd_workspace_bytes(ctypes.byref(dims)), dev)
+    _check(lib().gdr_linear_ce_fwd(_ptr(x), _ptr(weight), _ptr(targets), _ptr(loss), _ptr(lse), _ptr(ws),
+                                   0 if ws is None else ws.numel(), ctypes.byref(dims), _stream(x)))
+    return loss, lse
+
+
+def linear_ce_bwd(x, weight, targets, lse, dloss, *, workspace=None):
+    """Gradients of ``linear_ce_fwd`` (``gdr_linear_ce_bwd``): its inputs, the lse it returned and
+    dloss [N] fp32, the gradient of each token's loss. Returns (dx [N, D], dweight [V, D]) in x's dtype."""
+    dims, dev = _ce_args(x, weight, targets)
+    _need(lse, "lse", torch.float32, (dims.N,), dev)
+    _need(dloss, "dloss", torch.float32, (dims.N,), dev)
+    dx, dw = torch.empty_like(x), torch.empty_like(weight)
+    ws = _workspace(workspace, lib().gdr_linear_ce_bwd_workspace_bytes(ctypes.byref(dims)), dev)
+    _check(lib().gdr_linear_ce_bwd(_ptr(x), _ptr(weight), _ptr(targets), _ptr(lse), _ptr(dloss), _ptr(dx), _ptr(dw),
+                                   _ptr(ws), 0 if ws is None else ws.numel(), ctypes.byref(dims), _stream(x)))
+    return dx, dw
 
 
 def selftest_mfma(a, b):

@@ -20,7 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdr.so")
 
 SOURCES = ["gdr_api.cpp", "chunk_fwd.hip", "chunk_fwd_fast.hip", "decode.hip", "gdn2_fwd.hip", "gdn2_decode.hip", "bwd.hip",
-           "scratch.hip"]
+           "scratch.hip", "layer_api.cpp", "channel_scan.hip", "ffn.hip", "linear_ce.hip"]
 ARCH = os.environ.get("GDR_OFFLOAD_ARCH", "gfx950")
 
 

@@ -1,0 +1,134 @@
+// The gated feed-forward block on gfx950: both projections, the activation and the product in
+// one kernel, and the gradients.
+//
+//   G = x Wg^T,  U = x Wu^T,  h = act(G) * U
+//   dU = dh * act(G),  dG = dh * U * act'(G)
+//   dx = dG Wg + dU Wu,  dWg = dG^T x,  dWu = dU^T x
+//
+// Products are summed in 32 bits. With bf16 inputs G and U are kept in bf16 for the backward and
+// dG, dU enter its products in bf16: each is one rounding of a matrix operand, of the size of the
+// inputs' own.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdr_kernels.hpp"
+#include "layer_gemm.hpp"
+#include "layer_kernels.hpp"
+
+namespace gdr {
+
+namespace {
+
+constexpr float kGeluC = 0.7978845608028654f, kGeluA = 0.044715f;  // sqrt(2 / pi)
+
+__device__ __forceinline__ float sigmoid_f(float x) { return __builtin_amdgcn_rcpf(1.f + __expf(-x)); }
+
+// silu(x) = x sigmoid(x); gelu(x) = x sigmoid(2 c (x + a x^3)), the tanh form written as a sigmoid
+__device__ __forceinline__ float act_f(float x, int act) {
+    const float s = act == 0 ? x : 2.f * kGeluC * (x + kGeluA * x * x * x);
+    return x * sigmoid_f(s);
+}
+// the value and the derivative
+__device__ __forceinline__ void act_grad_f(float x, int act, float &val, float &der) {
+    const float s = act == 0 ? x : 2.f * kGeluC * (x + kGeluA * x * x * x);
+    const float ds = act == 0 ? 1.f : 2.f * kGeluC * (1.f + 3.f * kGeluA * x * x);
+    const float q = sigmoid_f(s);
+    val = x * q;
+    der = q + x * q * (1.f - q) * ds;
+}
+
+template <typename E>
+struct GluEpi {
+    E *h, *gate, *up;
+    int64_t M, F;
+    int act;
+    template <int MI, int NI>
+    __device__ __forceinline__ void operator()(const floatx4 (&acc)[2][MI][NI], int64_t m0, int64_t n0) const {
+        const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+        const bool wide = (F & 3) == 0;
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const int64_t m = m0 + 16 * i + c;
+            if (m >= M) continue;
+#pragma unroll
+            for (int j = 0; j < NI; ++j) {
+                const int64_t n = n0 + 16 * j + 4 * g;
+                if (n >= F) continue;
+                floatx4 v;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = act_f(acc[0][i][j][r], act) * acc[1][i][j][r];
+                store4(h + m * F + n, v, F - n, wide);
+                if (gate) {
+                    store4(gate + m * F + n, acc[0][i][j], F - n, wide);
+                    store4(up + m * F + n, acc[1][i][j], F - n, wide);
+                }
+            }
+        }
+    }
+};
+
+// dG and dU side by side, rows of ld elements, columns F .. ld-1 zero
+template <typename E>
+__global__ __launch_bounds__(256) void glu_grad_kernel(const E *gate, const E *up, const E *dh, E *dg, E *du, int64_t M,
+                                                       int64_t F, int64_t ld, int act) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= M * ld) return;
+    const int64_t m = i / ld, n = i % ld;
+    float vg = 0.f, vu = 0.f;
+    if (n < F) {
+        float val, der;
+        const int64_t k = m * F + n;
+        act_grad_f((float)gate[k], act, val, der);
+        const float d = (float)dh[k];
+        vg = d * (float)up[k] * der;
+        vu = d * val;
+    }
+    dg[i] = (E)vg;
+    du[i] = (E)vu;
+}
+
+int64_t grad_ld(int64_t F) { return (F + 7) / 8 * 8; }
+
+template <typename E>
+hipError_t fwd_t(const FfnArgs &a, hipStream_t s) {
+    AnyGemmArgs g{{a.x, nullptr}, {a.wg, a.wu}, a.D, 1, a.D, 1, a.M, a.F, a.D, 1};
+    return launch_gemm_any<E, 2>(g, GluEpi<E>{(E *)a.h, (E *)a.gate, (E *)a.up, a.M, a.F, a.act}, s);
+}
+
+template <typename E>
+hipError_t bwd_t(const FfnArgs &a, hipStream_t s) {
+    const int64_t ld = grad_ld(a.F);
+    E *dg = (E *)a.ws, *du = dg + a.M * ld;
+    if (a.M > 0) {
+        const int64_t blocks = (a.M * ld + 255) / 256;
+        hipLaunchKernelGGL((glu_grad_kernel<E>), dim3((unsigned)blocks), dim3(256), 0, s, (const E *)a.gate,
+                           (const E *)a.up, (const E *)a.dh, dg, du, a.M, a.F, ld, a.act);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        AnyGemmArgs gx{{dg, du}, {a.wg, a.wu}, ld, 1, 1, a.D, a.M, a.D, a.F, 2};
+        e = launch_gemm_any<E, 1>(gx, StoreEpi<E>{(E *)a.dx, nullptr, nullptr, a.M, a.D, a.D}, s);
+        if (e != hipSuccess) return e;
+    }
+    for (int i = 0; i < 2; ++i) {
+        AnyGemmArgs gw{{i ? du : dg, nullptr}, {a.x, nullptr}, 1, ld, 1, a.D, a.F, a.D, a.M, 1};
+        const hipError_t e =
+            launch_gemm_any<E, 1>(gw, StoreEpi<E>{(E *)(i ? a.dwu : a.dwg), nullptr, nullptr, a.F, a.D, a.D}, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+int64_t ffn_bwd_ws_bytes(int64_t M, int64_t, int64_t F, int dtype) {
+    return 2 * M * grad_ld(F) * (dtype == kDtypeBf16 ? 2 : 4);
+}
+
+hipError_t launch_ffn_fwd(const FfnArgs &a, int dtype, hipStream_t s) {
+    return dtype == kDtypeBf16 ? fwd_t<__bf16>(a, s) : fwd_t<float>(a, s);
+}
+hipError_t launch_ffn_bwd(const FfnArgs &a, int dtype, hipStream_t s) {
+    return dtype == kDtypeBf16 ? bwd_t<__bf16>(a, s) : bwd_t<float>(a, s);
+}
+
+}  // namespace gdr

@@ -7,9 +7,10 @@
 #include <stdint.h>
 #include <stdio.h>
 
+#include "gdr_host.hpp"
 #include "gdr_kernels.hpp"
 
-namespace {
+namespace gdr {
 
 thread_local char g_last_error[512] = "";
 
@@ -21,35 +22,18 @@ gdr_status_t fail(gdr_status_t s, const char *fmt, ...) {
     return s;
 }
 
-struct Range {
-    const char *name;
-    uintptr_t lo, hi;  // [lo, hi)
-    bool present() const { return lo != 0 && hi > lo; }
-};
+}  // namespace gdr
 
-Range rng(const char *name, const void *p, int64_t bytes) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{name, lo, lo + (uintptr_t)(bytes > 0 ? bytes : 0)};
-}
+using gdr::aligned;
+using gdr::elem_size;
+using gdr::fail;
+using gdr::g_last_error;
+using gdr::overlap;
+using gdr::prod;
+using gdr::Range;
+using gdr::rng;
 
-bool overlap(const Range &a, const Range &b) {
-    return a.present() && b.present() && a.lo < b.hi && b.lo < a.hi;
-}
-
-bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
-
-// product of non-negative sizes, or -1 on overflow past 2^62
-int64_t prod(std::initializer_list<int64_t> xs) {
-    int64_t r = 1;
-    for (int64_t x : xs) {
-        if (x < 0) return -1;
-        if (x != 0 && r > (INT64_C(1) << 62) / x) return -1;
-        r *= x;
-    }
-    return r;
-}
-
-int64_t elem_size(int32_t dtype) { return dtype == GDR_BF16 ? 2 : 4; }
+namespace {
 
 // The names the two gate arguments carry in messages.
 struct GateNames {

@@ -427,6 +427,168 @@ gdr_status_t gdr_gdn2_decode_step(const void *q, const void *k, const void *v,
                                   const float *state_in, float *state_out, void *out,
                                   const gdr_decode_dims_t *dims, void *stream);
 
+/*
+ * Layer operators: what stands next to the mixer in a recurrent model that is trained or served
+ * with this library. They follow the conventions above (device pointers, 16-byte aligned,
+ * contiguous; caller-owned workspaces; validation before anything is enqueued; no host read of
+ * device data). Every output is fully written, and the same inputs give the same bits.
+ *
+ * Channel scan: a gated linear recurrence with one number of state per channel. With the gates of
+ * the fused prologue, per channel d,
+ *
+ *   alpha_t = exp(-exp(A_log[d]) softplus(a_t + dt_bias[d])),   beta_t = sigmoid(b_t)
+ *   h_t = alpha_t h_{t-1} + beta_t x_t,   out_t = h_t
+ *
+ * The state, the gates and every sum are held in fp32; with bf16 inputs only `out` and the
+ * gradients of x, a and b are rounded, once.
+ */
+typedef struct gdr_scan_dims {
+    int64_t B;        /* batch rows; must be 1 when cu_seqlens is given */
+    int64_t T;        /* tokens per row (the packed total when cu_seqlens is given) */
+    int64_t D;        /* channels, >= 1 */
+    int64_t num_seqs; /* segments described by cu_seqlens (ignored when it is NULL) */
+    int32_t dtype;    /* gdr_dtype_t of x, a, b, out and their gradients */
+    uint32_t flags;   /* GDR_REVERSE: scan each sequence from its last token to its first */
+} gdr_scan_dims_t;
+
+/*
+ * gdr_channel_scan_fwd - the scan over whole sequences.
+ *
+ *   x, a, b      [B][T][D]  dtype
+ *   A_log, dt_bias [D]      fp32
+ *   h0           [S][D]     fp32 initial state per sequence, or NULL for zeros; S = B, or num_seqs
+ *   cu_seqlens   NULL, or DEVICE int32 [num_seqs + 1] as in gdr_chunk_fwd (empty segments allowed)
+ *   out          [B][T][D]  dtype
+ *   hT           [S][D]     fp32 final state, or NULL; may be exactly h0
+ *   states       fp32, gdr_channel_scan_states_elems(dims, packed) elements, or NULL: the state
+ *                entering every 256-token block of every sequence, which the backward needs
+ *   workspace    at least gdr_channel_scan_fwd_workspace_bytes(dims, packed) bytes (may be 0)
+ *
+ * Errors: GDR_ERR_NULL, GDR_ERR_DIMS (sizes, or a workspace that is too small), GDR_ERR_DTYPE,
+ * GDR_ERR_ALIGN, GDR_ERR_ALIAS (an output overlapping an input or another output), GDR_ERR_FLAGS,
+ * GDR_ERR_HIP. The size functions return -1 for sizes the call would refuse.
+ */
+int64_t gdr_channel_scan_states_elems(const gdr_scan_dims_t *dims, int32_t packed);
+int64_t gdr_channel_scan_fwd_workspace_bytes(const gdr_scan_dims_t *dims, int32_t packed);
+gdr_status_t gdr_channel_scan_fwd(const void *x, const void *a, const void *b, const float *A_log,
+                                  const float *dt_bias, const float *h0, const int32_t *cu_seqlens,
+                                  void *out, float *hT, float *states, void *workspace,
+                                  int64_t workspace_bytes, const gdr_scan_dims_t *dims, void *stream);
+
+/*
+ * gdr_channel_scan_bwd - gradients of sum(out * dout) + sum(hT * dhT) with respect to every input
+ * of the forward.
+ *
+ *   x, a, b, A_log, dt_bias, cu_seqlens, dims: as given to the forward; states: as it wrote them
+ *   dout         [B][T][D]  dtype
+ *   dhT          [S][D]     fp32, or NULL for zero
+ *   dx, da, db   [B][T][D]  dtype
+ *   dA_log, ddt_bias [D]    fp32
+ *   dh0          [S][D]     fp32, or NULL when not wanted
+ *   workspace    at least gdr_channel_scan_bwd_workspace_bytes(dims, packed) bytes
+ *
+ * Errors as the forward.
+ */
+int64_t gdr_channel_scan_bwd_workspace_bytes(const gdr_scan_dims_t *dims, int32_t packed);
+gdr_status_t gdr_channel_scan_bwd(const void *x, const void *a, const void *b, const float *A_log,
+                                  const float *dt_bias, const float *states,
+                                  const int32_t *cu_seqlens, const void *dout, const float *dhT,
+                                  void *dx, void *da, void *db, float *dA_log, float *ddt_bias,
+                                  float *dh0, void *workspace, int64_t workspace_bytes,
+                                  const gdr_scan_dims_t *dims, void *stream);
+
+/*
+ * gdr_channel_scan_step - one token for B independent sequences (T must be 1, no flags).
+ *
+ *   x, a, b, out [B][D] dtype;  state_in, state_out [B][D] fp32 (state_out may be exactly state_in)
+ *
+ * Errors as the forward.
+ */
+gdr_status_t gdr_channel_scan_step(const void *x, const void *a, const void *b, const float *A_log,
+                                   const float *dt_bias, const float *state_in, float *state_out,
+                                   void *out, const gdr_scan_dims_t *dims, void *stream);
+
+/*
+ * Gated feed-forward block, up to its down projection:
+ *
+ *   G = x w_gate^T,  U = x w_up^T,  h = act(G) * U
+ *
+ * with act silu, G sigmoid(G), or the tanh form of gelu.
+ */
+typedef enum gdr_act { GDR_ACT_SILU = 0, GDR_ACT_GELU_TANH = 1 } gdr_act_t;
+
+typedef struct gdr_ffn_dims {
+    int64_t M;     /* tokens, >= 0 */
+    int64_t D;     /* input width, 1 .. 2^20 */
+    int64_t F;     /* hidden width, 1 .. 2^20 */
+    int32_t dtype; /* gdr_dtype_t of every tensor */
+    int32_t act;   /* gdr_act_t */
+} gdr_ffn_dims_t;
+
+/*
+ * gdr_gated_ffn_fwd - both projections, the activation and the product in one kernel.
+ *
+ *   x [M][D];  w_gate, w_up [F][D];  h [M][F]
+ *   gate, up [M][F]: G and U, kept (in dtype) for the backward; both NULL when not wanted
+ *
+ * gdr_gated_ffn_bwd - gradients of sum(h * dh): dx [M][D], dw_gate and dw_up [F][D], from x, the
+ * weights, gate and up as the forward kept them and dh [M][F]; every tensor in dtype. workspace: at
+ * least gdr_gated_ffn_bwd_workspace_bytes(dims) bytes.
+ *
+ * Products are summed in fp32. With bf16 inputs G and U are rounded to bf16 where they are kept
+ * (h itself is formed from the unrounded ones), and dG and dU where they enter the backward's
+ * products. Rows of any width are taken; D a multiple of 16 bytes is the fast case.
+ * Errors as gdr_channel_scan_fwd; GDR_ERR_FLAGS for an unknown act.
+ */
+gdr_status_t gdr_gated_ffn_fwd(const void *x, const void *w_gate, const void *w_up, void *h,
+                               void *gate, void *up, const gdr_ffn_dims_t *dims, void *stream);
+int64_t gdr_gated_ffn_bwd_workspace_bytes(const gdr_ffn_dims_t *dims);
+gdr_status_t gdr_gated_ffn_bwd(const void *x, const void *w_gate, const void *w_up,
+                               const void *gate, const void *up, const void *dh, void *dx,
+                               void *dw_gate, void *dw_up, void *workspace, int64_t workspace_bytes,
+                               const gdr_ffn_dims_t *dims, void *stream);
+
+/*
+ * Softmax cross entropy of a linear layer over a vocabulary, the logits never kept:
+ *
+ *   l = x w^T,   lse_n = log sum_v exp(l_nv),   loss_n = lse_n - l_{n, targets[n]}
+ */
+typedef struct gdr_ce_dims {
+    int64_t N;      /* tokens, >= 0 */
+    int64_t D;      /* width, 1 .. 2^20 */
+    int64_t V;      /* vocabulary, >= 1 */
+    int32_t dtype;  /* gdr_dtype_t of x, w, dx and dw */
+    uint32_t flags; /* 0 */
+} gdr_ce_dims_t;
+
+/*
+ * gdr_linear_ce_fwd - the loss of every token.
+ *
+ *   x [N][D], w [V][D] dtype;  targets [N] int64 (DEVICE); loss, lse [N] fp32
+ *
+ * A token whose target is outside 0 .. V-1 bears no loss (0) and no gradient; its lse is written
+ * all the same. The logits stay in fp32 and are reduced to a partial sum per token as they are
+ * formed.
+ *
+ * gdr_linear_ce_bwd - gradients of sum(loss * dloss): dx [N][D] and dw [V][D] in dtype, from lse as
+ * the forward wrote it and dloss [N] fp32 (not read where the target is outside the vocabulary).
+ * The logits are formed again, one piece of the vocabulary after another; with bf16 inputs a
+ * piece's gradient is rounded to bf16 as an operand of the two products, dx is summed over the
+ * pieces in fp32.
+ *
+ * workspace: at least gdr_linear_ce_{fwd,bwd}_workspace_bytes(dims) bytes.
+ * Errors as gdr_channel_scan_fwd.
+ */
+int64_t gdr_linear_ce_fwd_workspace_bytes(const gdr_ce_dims_t *dims);
+gdr_status_t gdr_linear_ce_fwd(const void *x, const void *w, const int64_t *targets, float *loss,
+                               float *lse, void *workspace, int64_t workspace_bytes,
+                               const gdr_ce_dims_t *dims, void *stream);
+int64_t gdr_linear_ce_bwd_workspace_bytes(const gdr_ce_dims_t *dims);
+gdr_status_t gdr_linear_ce_bwd(const void *x, const void *w, const int64_t *targets,
+                               const float *lse, const float *dloss, void *dx, void *dw,
+                               void *workspace, int64_t workspace_bytes, const gdr_ce_dims_t *dims,
+                               void *stream);
+
 /* Static text for a status code. */
 const char *gdr_status_string(gdr_status_t status);
 
