@@ -91,8 +91,8 @@ int64_t grad_ld(int64_t F) { return (F + 7) / 8 * 8; }
 
 template <typename E>
 hipError_t fwd_t(const FfnArgs &a, hipStream_t s) {
-    AnyGemmArgs g{{a.x, nullptr}, {a.wg, a.wu}, a.D, 1, a.D, 1, a.M, a.F, a.D, 1};
-    return launch_gemm_any<E, 2>(g, GluEpi<E>{(E *)a.h, (E *)a.gate, (E *)a.up, a.M, a.F, a.act}, s);
+    const GemmOp g{{a.x, nullptr}, {a.wg, a.wu}, a.D, a.D, a.M, a.F, a.D, 1};
+    return launch_gemm<E, true, true, 2>(g, GluEpi<E>{(E *)a.h, (E *)a.gate, (E *)a.up, a.M, a.F, a.act}, s);
 }
 
 template <typename E>
@@ -105,14 +105,14 @@ hipError_t bwd_t(const FfnArgs &a, hipStream_t s) {
                            (const E *)a.up, (const E *)a.dh, dg, du, a.M, a.F, ld, a.act);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        AnyGemmArgs gx{{dg, du}, {a.wg, a.wu}, ld, 1, 1, a.D, a.M, a.D, a.F, 2};
-        e = launch_gemm_any<E, 1>(gx, StoreEpi<E>{(E *)a.dx, nullptr, nullptr, a.M, a.D, a.D}, s);
+        const GemmOp gx{{dg, du}, {a.wg, a.wu}, ld, a.D, a.M, a.D, a.F, 2};
+        e = launch_gemm<E, true, false, 1>(gx, StoreEpi<E>{(E *)a.dx, nullptr, nullptr, a.M, a.D, a.D}, s);
         if (e != hipSuccess) return e;
     }
     for (int i = 0; i < 2; ++i) {
-        AnyGemmArgs gw{{i ? du : dg, nullptr}, {a.x, nullptr}, 1, ld, 1, a.D, a.F, a.D, a.M, 1};
+        const GemmOp gw{{i ? du : dg, nullptr}, {a.x, nullptr}, ld, a.D, a.F, a.D, a.M, 1};
         const hipError_t e =
-            launch_gemm_any<E, 1>(gw, StoreEpi<E>{(E *)(i ? a.dwu : a.dwg), nullptr, nullptr, a.F, a.D, a.D}, s);
+            launch_gemm<E, false, false, 1>(gw, StoreEpi<E>{(E *)(i ? a.dwu : a.dwg), nullptr, nullptr, a.F, a.D, a.D}, s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

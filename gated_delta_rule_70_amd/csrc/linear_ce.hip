@@ -23,7 +23,11 @@ namespace gdr {
 
 namespace {
 
-constexpr int kStrip = 32;  // vocabulary columns per partial sum
+// vocabulary columns per partial sum: those of one wave of the product
+template <typename E>
+int64_t strip_of(int64_t D) {
+    return whole_pieces<E>(D) ? kTileCols : kAnyCols;
+}
 
 struct StatEpi {
     const int64_t *t;
@@ -57,7 +61,7 @@ struct StatEpi {
                     if (n0 + 16 * j + 4 * g + r < V) sum += __expf(acc[0][i][j][r] - ref);
             sum += __shfl_xor(sum, 16, 64);
             sum += __shfl_xor(sum, 32, 64);
-            if (g == 0 && m < M) part[(n0 / kStrip) * M + m] = make_float2(top, sum);
+            if (g == 0 && m < M) part[(n0 / (16 * NI)) * M + m] = make_float2(top, sum);
         }
     }
 };
@@ -113,7 +117,10 @@ __global__ __launch_bounds__(64) void ce_join_kernel(const float2 *part, const f
 }
 
 int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
-int64_t strips_of(int64_t V) { return (V + kStrip - 1) / kStrip; }
+template <typename E>
+int64_t strips_of(int64_t D, int64_t V) {
+    return (V + strip_of<E>(D) - 1) / strip_of<E>(D);
+}
 
 // Vocabulary columns per piece of the backward: dl of a piece takes at most about 512 MB.
 int64_t piece_of(int64_t N, int64_t V) {
@@ -126,11 +133,11 @@ int64_t piece_of(int64_t N, int64_t V) {
 template <typename E>
 hipError_t fwd_t(const CeArgs &a, hipStream_t s) {
     if (a.N == 0) return hipSuccess;
-    const int64_t strips = strips_of(a.V);
+    const int64_t strips = strips_of<E>(a.D, a.V);
     float *tgt = (float *)a.ws;
     float2 *part = (float2 *)((char *)a.ws + up256(a.N * 4));
-    AnyGemmArgs g{{a.x, nullptr}, {a.w, nullptr}, a.D, 1, a.D, 1, a.N, a.V, a.D, 1};
-    const hipError_t e = launch_gemm_any<E, 1>(g, StatEpi{a.t, part, tgt, a.N, a.V}, s);
+    const GemmOp g{{a.x, nullptr}, {a.w, nullptr}, a.D, a.D, a.N, a.V, a.D, 1};
+    const hipError_t e = launch_gemm<E, true, true, 1>(g, StatEpi{a.t, part, tgt, a.N, a.V}, s);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(ce_join_kernel, dim3((unsigned)((a.N + 63) / 64)), dim3(64), 0, s, part, tgt, a.t, a.loss, a.lse,
                        a.N, a.V, strips);
@@ -145,16 +152,16 @@ hipError_t bwd_t(const CeArgs &a, hipStream_t s) {
     for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
         const int64_t width = a.V - v0 < piece ? a.V - v0 : piece;
         const E *w = (const E *)a.w + v0 * a.D;
-        AnyGemmArgs gl{{a.x, nullptr}, {w, nullptr}, a.D, 1, a.D, 1, a.N, width, a.D, 1};
-        hipError_t e = launch_gemm_any<E, 1>(
+        const GemmOp gl{{a.x, nullptr}, {w, nullptr}, a.D, a.D, a.N, width, a.D, 1};
+        hipError_t e = launch_gemm<E, true, true, 1>(
             gl, GradEpi<E>{a.t, a.lse_in, a.dloss, dl, a.N, a.V, v0, width, piece}, s);
         if (e != hipSuccess) return e;
-        AnyGemmArgs gw{{dl, nullptr}, {a.x, nullptr}, 1, piece, 1, a.D, width, a.D, a.N, 1};
-        e = launch_gemm_any<E, 1>(gw, StoreEpi<E>{(E *)a.dw + v0 * a.D, nullptr, nullptr, width, a.D, a.D}, s);
+        const GemmOp gw{{dl, nullptr}, {a.x, nullptr}, piece, a.D, width, a.D, a.N, 1};
+        e = launch_gemm<E, false, false, 1>(gw, StoreEpi<E>{(E *)a.dw + v0 * a.D, nullptr, nullptr, width, a.D, a.D}, s);
         if (e != hipSuccess) return e;
         const bool last = v0 + piece >= a.V;
-        AnyGemmArgs gx{{dl, nullptr}, {w, nullptr}, piece, 1, 1, a.D, a.N, a.D, width, 1};
-        e = launch_gemm_any<E, 1>(
+        const GemmOp gx{{dl, nullptr}, {w, nullptr}, piece, a.D, a.N, a.D, width, 1};
+        e = launch_gemm<E, true, false, 1>(
             gx, StoreEpi<E>{last ? (E *)a.dx : nullptr, v0 ? acc : nullptr, acc, a.N, a.D, a.D}, s);
         if (e != hipSuccess) return e;
     }
@@ -163,7 +170,10 @@ hipError_t bwd_t(const CeArgs &a, hipStream_t s) {
 
 }  // namespace
 
-int64_t ce_fwd_ws_bytes(int64_t N, int64_t, int64_t V, int) { return up256(N * 4) + strips_of(V) * N * 8; }
+int64_t ce_fwd_ws_bytes(int64_t N, int64_t D, int64_t V, int dtype) {
+    const int64_t strips = dtype == kDtypeBf16 ? strips_of<__bf16>(D, V) : strips_of<float>(D, V);
+    return up256(N * 4) + strips * N * 8;
+}
 int64_t ce_bwd_ws_bytes(int64_t N, int64_t D, int64_t V, int dtype) {
     const int64_t piece = piece_of(N, V);
     return up256(N * piece * (dtype == kDtypeBf16 ? 2 : 4)) + (piece < V ? N * D * 4 : 0);
