@@ -36,15 +36,21 @@ def _flags():
     return ["-O3", "-std=c++17", "-fPIC", "--offload-arch=%s" % ARCH,
             # packed fp32 instructions are switched off for all device code
             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-            # matrix-core accumulators in ordinary VGPRs: the kernels apply VALU ops to
-            # them every chunk, and AGPR accumulators would need a move each way
-            "-mllvm", "-amdgpu-mfma-vgpr-form",
             "-I", INCLUDE, "-I", CSRC, "-Wall", "-Wno-unused-function"]
+
+
+def _source_flags(src: str):
+    # the matrix products of these sources keep 256 accumulators a lane, in AGPRs
+    if src in ("ffn.hip", "linear_ce.hip"):
+        return []
+    # matrix-core accumulators in ordinary VGPRs: the kernels apply VALU ops to
+    # them every chunk, and AGPR accumulators would need a move each way
+    return ["-mllvm", "-amdgpu-mfma-vgpr-form"]
 
 
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-    cmd = [hipcc()] + _flags() + ["-x", "hip", "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [hipcc()] + _flags() + _source_flags(src) + ["-x", "hip", "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     noise = "is not a recognized feature for this target"
     err = "\n".join(l for l in r.stderr.splitlines() if noise not in l)

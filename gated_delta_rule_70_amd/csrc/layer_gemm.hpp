@@ -96,7 +96,7 @@ hipError_t launch_gemm_any(const AnyGemmArgs &a, const Epi &epi, hipStream_t s) 
 //
 // A workgroup of WM x WN waves computes BM x (BN / NB) columns of C; a block of 128 bytes of k (64 bf16
 // or 32 fp32) of both operands is copied straight from global memory into one half of LDS while
-// the other half is multiplied: one barrier a block, one block of latency hidden. An operand
+// the other half is multiplied, one barrier a block. An operand
 // comes in either order:
 //   KC (k contiguous, rows of ld elements): LDS holds rows of 128 bytes, eight 16-byte pieces, piece p
 //      of row r at p ^ (r & 7), so that the 16 rows a fragment read touches spread over the banks;
@@ -134,12 +134,18 @@ __device__ __forceinline__ void copy_b128(unsigned lds, u32x4 rsrc, int voff) {
 }
 __device__ __forceinline__ u32x4 buffer_at(const char *p, int64_t bytes) {
     const uint64_t a = reinterpret_cast<uint64_t>(p);
-    const unsigned n = bytes > 0x7fffffff ? 0x7fffffffu : bytes < 0 ? 0u : (unsigned)bytes;
+    // bytes clamped to 0 .. 2^31 - 1, in 32-bit halves (there is no scalar 64-bit less-than)
+    const int hi = (int)(bytes >> 32);
+    const unsigned lo = (unsigned)bytes;
+    const unsigned n = hi < 0 ? 0u : hi > 0 || lo > 0x7fffffffu ? 0x7fffffffu : lo;
     u32x4 r;
     r.x = __builtin_amdgcn_readfirstlane((unsigned)a);
     r.y = __builtin_amdgcn_readfirstlane((unsigned)(a >> 32) & 0xffffu);
     r.z = __builtin_amdgcn_readfirstlane(n);
     r.w = 0x00020000;  // raw, untyped
+    // A vector instruction's write of a scalar register (readfirstlane) needs five wait states before
+    // a buffer access reads it; the compiler does not count them for an access inside assembly.
+    asm volatile("s_nop 4" : "+s"(r));
     return r;
 }
 
@@ -185,12 +191,18 @@ struct Operand {
             }
         }
     }
-    // block kb of the operand into LDS at `lds` (byte address)
-    __device__ __forceinline__ void copy(const char *b, int kb, unsigned lds, int wave) const {
-        const u32x4 r = buffer_at(b + kb * step, limit - kb * step);
-        const bool in = !KC || (int64_t)kb * 128 + kpiece < kbytes;
-#pragma unroll
-        for (int i = 0; i < L; ++i) copy_b128(lds + (wave * L + i) * 1024, r, in ? voff[i] : 0x7fffffff);
+    // Block kb of the operand, this wave's copy i into LDS at `lds` (byte address). A block past the
+    // last reads nothing: in the k-strided order its descriptor holds no bytes (kb KB >= K rows of
+    // ld >= rows - r0 elements lie behind it), in the k-contiguous one each piece begins past the
+    // row's end.
+    u32x4 rsrc;
+    bool in;
+    __device__ __forceinline__ void begin(const char *b, int kb) {
+        rsrc = buffer_at(b + kb * step, limit - kb * step);
+        in = !KC || (int64_t)kb * 128 + kpiece < kbytes;
+    }
+    __device__ __forceinline__ void copy(int i, unsigned lds, int wave) const {
+        copy_b128(lds + (wave * L + i) * 1024, rsrc, in ? voff[i] : 0x7fffffff);
     }
 };
 
@@ -252,8 +264,15 @@ __device__ __forceinline__ floatx4 mma_step(floatx4 acc, bf16x8 a, bf16x8 b) {
 }
 __device__ __forceinline__ floatx4 mma_step(floatx4 acc, floatx4 a, floatx4 b) { return mma16(acc, a, b); }
 
+// The same with the accumulator held to AGPRs: left to itself the compiler moved a quarter of the
+// large tile's 256 accumulators between register files in every block (588 instructions a block
+// next to 128 matrix ones; 330 this way).
+__device__ __forceinline__ void mma_step_agpr(floatx4 &acc, bf16x8 a, bf16x8 b) {
+    asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+}
+
 template <typename E, bool AKC, bool BKC, int NB, int BM, int BN, int WM, int WN, class Epi>
-__global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(TileGemmArgs a, Epi epi) {
+__global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 : 2) void gemm_tile_kernel(TileGemmArgs a, Epi epi) {
     constexpr int NW = WM * WN, TM = BM / WM, TN = BN / NB / WN, MI = TM / 16, NI = TN / 16, KB = 128 / (int)sizeof(E);
     static_assert(NB == 1 || BKC, "two B matrices come k contiguous");
     __shared__ __align__(1024) char lds[2][(BM + BN) * 128];
@@ -276,25 +295,39 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(TileGemmArgs
     Operand<E, BKC, BN / NB, NW / NB> B;
     const int bhalf = NB == 2 ? wave / (NW / 2) : 0, bwave = NB == 2 ? wave % (NW / 2) : wave;
     B.init(a.B[bhalf], a.ldb, n0, a.N, a.K, bwave, lane);
-    const char *abase2 = A.base + ((const char *)a.A[1] - (const char *)a.A[0]);
-    const char *bbase2 = B.base + ((const char *)a.B[1] - (const char *)a.B[0]);
+    // the second pair of a sum of two products (never with two B matrices)
+    const bool two = NB == 1 && a.pairs == 2;
+    const char *abase2 = two ? A.base + ((const char *)a.A[1] - (const char *)a.A[0]) : A.base;
+    const char *bbase2 = two ? B.base + ((const char *)a.B[1] - (const char *)a.B[0]) : B.base;
 
     Fragments<E, AKC, BM, MI> fa;
     Fragments<E, BKC, BN / NB, NI> fb;
     fa.init(wm * TM, lane);
     fb.init(wn * TN, lane);
 
-    const int nkb = (int)((a.K + KB - 1) / KB), total_kb = nkb * a.pairs;
+    const int nkb = (int)((a.K + KB - 1) / KB), total_kb = two ? 2 * nkb : nkb;
     const unsigned lds0 = __builtin_amdgcn_readfirstlane(
         (unsigned)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char *)&lds[0][0]));
-    auto copy = [&](int kb) {
-        const unsigned at = lds0 + (kb & 1) * (BM + BN) * 128;
-        const bool second = kb >= nkb;
+    constexpr int LA = Operand<E, AKC, BM, NW>::L, LB = Operand<E, BKC, BN / NB, NW / NB>::L;
+    auto begin_copy = [&](int kb) {
+        const bool second = two && kb >= nkb;
         const int k = second ? kb - nkb : kb;
-        A.copy(second ? abase2 : A.base, k, at, wave);
-        B.copy(second ? bbase2 : B.base, k, at + BM * 128 + bhalf * (BN / NB) * 128, bwave);
+        A.begin(second ? abase2 : A.base, k);
+        B.begin(second ? bbase2 : B.base, k);
+    };
+    // this wave's copies i0 .. i1 - 1 of the LA + LB of block kb
+    auto copy = [&](int kb, int i0, int i1) {
+        const unsigned at = lds0 + (kb & 1) * (BM + BN) * 128;
+#pragma unroll
+        for (int i = 0; i < LA + LB; ++i)
+            if (i >= i0 && i < i1) {
+                if (i < LA) A.copy(i, at, wave);
+                else B.copy(i - LA, at + BM * 128 + bhalf * (BN / NB) * 128, bwave);
+            }
     };
 
+    // 256 accumulators a lane are the AGPRs
+    constexpr bool in_agprs = NB * MI * NI > 32;
     floatx4 acc[NB][MI][NI];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -313,30 +346,58 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(TileGemmArgs
 #pragma unroll
                 for (int j = 0; j < NI; ++j) total[b][i][j] = zero4();
 
-    if (total_kb > 0) copy(0);
-    for (int kb = 0; kb < total_kb; ++kb) {
-        // this wave's copies of block kb have landed and its reads of block kb - 1 are done
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        if (kb + 1 < total_kb) copy(kb + 1);
+    // fragments of the two halves of a block
+    typename Fragments<E, AKC, BM, MI>::type va[2][MI], vb[2][NB * NI];
+    // reads i0 .. i1 - 1 of the NB NI + MI of half ks of block kb
+    auto read = [&](int kb, int ks, int i0, int i1) {
         const char *buf = lds[kb & 1];
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            typename Fragments<E, AKC, BM, MI>::type va[MI], vb[NB][NI];
+        for (int i = 0; i < NB * NI + MI; ++i)
+            if (i >= i0 && i < i1) {
+                if (i < NB * NI) vb[ks][i] = fb.read(buf + BM * 128 + (i / NI) * (BN / NB) * 128, i % NI, ks);
+                else va[ks][i - NB * NI] = fa.read(buf, i - NB * NI, ks);
+            }
+    };
+    // Multiplies half ks row by row of the wave's tiles; `side(i)` is issued before row i, in the
+    // shadow of the matrix instructions of the row before.
+    auto multiply = [&](int ks, auto side) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            side(i);
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int j = 0; j < NI; ++j) vb[b][j] = fb.read(buf + BM * 128 + b * (BN / NB) * 128, j, ks);
-#pragma unroll
-            for (int i = 0; i < MI; ++i) va[i] = fa.read(buf, i, ks);
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int j = 0; j < NI; ++j) acc[b][i][j] = mma_step(acc[b][i][j], vb[b][j], va[i]);
+                for (int j = 0; j < NI; ++j) {
+                    if constexpr (in_agprs) mma_step_agpr(acc[b][i][j], vb[ks][b * NI + j], va[ks][i]);
+                    else acc[b][i][j] = mma_step(acc[b][i][j], vb[ks][b * NI + j], va[ks][i]);
+                }
+            __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    // this wave's copies have landed and its reads of the block in use are done, then everyone's
+    auto hand_over = [] {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    // The first half of a block is multiplied while its second half is read from LDS; then the halves
+    // of LDS change hands, and the second half is multiplied while the next block's first is read
+    // and the block after it is copied in.
+    constexpr int NR = NB * NI + MI, NC = LA + LB;
+    begin_copy(0);
+    copy(0, 0, NC);
+    hand_over();
+    begin_copy(1);
+    copy(1, 0, NC);
+    read(0, 0, 0, NR);
+    for (int kb = 0; kb < total_kb; ++kb) {
+        multiply(0, [&](int i) { read(kb, 1, i * NR / MI, (i + 1) * NR / MI); });
+        hand_over();
+        begin_copy(kb + 2);
+        multiply(1, [&](int i) {
+            read(kb + 1, 0, i * NR / MI, (i + 1) * NR / MI);
+            copy(kb + 2, i * NC / MI, (i + 1) * NC / MI);
+        });
         if constexpr (blocked)
             if ((kb + 1) % (kSumK / KB) == 0) {
 #pragma unroll
@@ -350,6 +411,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(TileGemmArgs
                         }
             }
     }
+    // the copies past the end land before the wave ends
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     if constexpr (blocked)
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -357,6 +420,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(TileGemmArgs
             for (int i = 0; i < MI; ++i)
 #pragma unroll
                 for (int j = 0; j < NI; ++j) acc[b][i][j] += total[b][i][j];
+    // matrix results are read by other instructions from here on: 18 wait states
+    if constexpr (in_agprs) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NI; ++j) asm volatile("" : "+a"(acc[b][i][j]));
+        asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+    }
     epi(acc, m0 + wm * TM, n0 + wn * TN);
 }
 
@@ -364,7 +437,7 @@ template <typename E, bool AKC, bool BKC, int NB, int BM, int BN, int WM, int WN
 hipError_t launch_gemm_tile(TileGemmArgs a, const Epi &epi, hipStream_t s) {
     const int64_t nm = (a.M + BM - 1) / BM, nn = (a.N + BN / NB - 1) / (BN / NB);
     if (nm * nn == 0) return hipSuccess;
-    if (nm * nn > INT32_MAX / 16) return hipErrorInvalidValue;
+    if (nm * nn > INT32_MAX / 16 || a.pairs < 1 || a.pairs > 3 - NB) return hipErrorInvalidValue;
     a.nm = (int)nm;
     a.nn = (int)nn;
     hipLaunchKernelGGL((gemm_tile_kernel<E, AKC, BKC, NB, BM, BN, WM, WN, Epi>), dim3((unsigned)(nm * nn)),
@@ -372,7 +445,7 @@ hipError_t launch_gemm_tile(TileGemmArgs a, const Epi &epi, hipStream_t s) {
     return hipGetLastError();
 }
 
-// columns of C per wave of launch_gemm's kernels
+// columns of C per wave are a multiple of this in the tiled and in the any-size kernel
 constexpr int kTileCols = 64, kAnyCols = 32;
 
 // C = sum of A_p B_p^T in the order given by AKC and BKC (true: k contiguous, the leading dimension
@@ -393,7 +466,7 @@ hipError_t launch_gemm(const GemmOp &o, const Epi &epi, hipStream_t s) {
         TileGemmArgs t{{o.A[0], o.A[1] ? o.A[1] : o.A[0]}, {o.B[0], o.B[1] ? o.B[1] : o.B[0]}, o.lda, o.ldb, o.M, o.N, o.K, o.pairs, 0, 0};
         const int64_t big = ((o.M + 255) / 256) * ((o.N * NB + 255) / 256);
         if constexpr (sizeof(E) == 2)
-            if (big >= 192) return launch_gemm_tile<E, AKC, BKC, NB, 256, 256, 2, 4>(t, epi, s);
+            if (big >= 192) return launch_gemm_tile<E, AKC, BKC, NB, 256, 256, 2, 2>(t, epi, s);
         return launch_gemm_tile<E, AKC, BKC, NB, 128, 128, 2, 2>(t, epi, s);
     }
     AnyGemmArgs g{{o.A[0], o.A[1]}, {o.B[0], o.B[1]}, AKC ? o.lda : 1, AKC ? 1 : o.lda, BKC ? o.ldb : 1, BKC ? 1 : o.ldb,

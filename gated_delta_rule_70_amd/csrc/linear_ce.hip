@@ -23,7 +23,7 @@ namespace gdr {
 
 namespace {
 
-// vocabulary columns per partial sum: those of one wave of the product
+// vocabulary columns per partial sum
 template <typename E>
 int64_t strip_of(int64_t D) {
     return whole_pieces<E>(D) ? kTileCols : kAnyCols;
@@ -36,32 +36,39 @@ struct StatEpi {
     int64_t M, V;
     template <int MI, int NI>
     __device__ __forceinline__ void operator()(const floatx4 (&acc)[1][MI][NI], int64_t m0, int64_t n0) const {
+        constexpr int SJ = NI < kTileCols / 16 ? NI : kTileCols / 16;  // tiles per strip
         const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-        if (n0 >= V) return;
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             const int64_t m = m0 + 16 * i + c;
             const int64_t tm = m < M ? t[m] : -1;
-            float top = -INFINITY, sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < NI; ++j)
+            for (int s = 0; s < NI / SJ; ++s) {
+                const int64_t ns = n0 + 16 * SJ * s;
+                if (ns >= V) continue;
+                const int left = V - ns < 16 * SJ ? (int)(V - ns) : 16 * SJ;        // columns in range
+                const int want = tm >= ns && tm < ns + left ? (int)(tm - ns) : -1;  // the target's column
+                float top = -INFINITY, sum = 0.f;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int64_t n = n0 + 16 * j + 4 * g + r;
-                    if (n < V) top = fmaxf(top, acc[0][i][j][r]);
-                    if (n == tm) tgt[m] = acc[0][i][j][r];
-                }
-            top = fmaxf(top, __shfl_xor(top, 16, 64));
-            top = fmaxf(top, __shfl_xor(top, 32, 64));
-            const float ref = top == -INFINITY ? 0.f : top;
+                for (int j = 0; j < SJ; ++j)
 #pragma unroll
-            for (int j = 0; j < NI; ++j)
+                    for (int r = 0; r < 4; ++r) {
+                        const int n = 16 * j + 4 * g + r;
+                        if (n < left) top = fmaxf(top, acc[0][i][SJ * s + j][r]);
+                        if (n == want) tgt[m] = acc[0][i][SJ * s + j][r];
+                    }
+                top = fmaxf(top, __shfl_xor(top, 16, 64));
+                top = fmaxf(top, __shfl_xor(top, 32, 64));
+                const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (n0 + 16 * j + 4 * g + r < V) sum += __expf(acc[0][i][j][r] - ref);
-            sum += __shfl_xor(sum, 16, 64);
-            sum += __shfl_xor(sum, 32, 64);
-            if (g == 0 && m < M) part[(n0 / (16 * NI)) * M + m] = make_float2(top, sum);
+                for (int j = 0; j < SJ; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (16 * j + 4 * g + r < left) sum += __expf(acc[0][i][SJ * s + j][r] - ref);
+                sum += __shfl_xor(sum, 16, 64);
+                sum += __shfl_xor(sum, 32, 64);
+                if (g == 0 && m < M) part[(ns / (16 * SJ)) * M + m] = make_float2(top, sum);
+            }
         }
     }
 };
@@ -83,15 +90,19 @@ struct GradEpi {
             const int64_t tm = t[m];
             const bool on = tm >= 0 && tm < V;
             const float ls = lse[m], sc = on ? dloss[m] : 0.f;
+            // the target's column and the piece's end, from this wave's first column
+            const int want = tm - v0 >= n0 && tm - v0 < n0 + 16 * NI ? (int)(tm - v0 - n0) : -1;
+            const int left = !on ? 0 : width - n0 < 16 * NI ? (int)(width - n0) : 16 * NI;
 #pragma unroll
             for (int j = 0; j < NI; ++j) {
-                const int64_t n = n0 + 16 * j + 4 * g;
+                const int k = 16 * j + 4 * g;
+                const int64_t n = n0 + k;
                 if (n >= ld) continue;
                 floatx4 v;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float p = __expf(acc[0][i][j][r] - ls) - (v0 + n + r == tm ? 1.f : 0.f);
-                    v[r] = on && n + r < width ? p * sc : 0.f;
+                    const float p = __expf(acc[0][i][j][r] - ls) - (k + r == want ? 1.f : 0.f);
+                    v[r] = k + r < left ? p * sc : 0.f;
                 }
                 store4(dl + m * ld + n, v, ld - n, true);
             }

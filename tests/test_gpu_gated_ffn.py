@@ -78,6 +78,12 @@ def test_large_tiles_ragged(gdr, dtype):
     compare(gdr, 2049, 264, 515, dtype)
 
 
+@pytest.mark.parametrize("M,D,F", [(4097, 72, 1601), (4097, 3336, 24), (33, 3600, 3592)])
+def test_large_outputs(gdr, M, D, F):
+    """Wide in turn in each product's result: h and its projections, dx, and the weights' gradients."""
+    compare(gdr, M, D, F, BF16)
+
+
 def test_no_tokens(gdr):
     x, wg, wu, _ = (t.cuda() for t in make(3, 32, 48, BF16, 2))
     e, eh = x[:0], torch.empty(0, 48, dtype=BF16, device="cuda")

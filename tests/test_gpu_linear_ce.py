@@ -80,6 +80,12 @@ def test_large_tiles_ragged(gdr, dtype):
     compare(gdr, 1100, 264, 3001, dtype)
 
 
+@pytest.mark.parametrize("N,D,V", [(4097, 72, 3201), (4097, 3336, 40), (40, 3600, 3593)])
+def test_large_outputs(gdr, N, D, V):
+    """Wide in turn in each product's result: the logits, dx and dw."""
+    compare(gdr, N, D, V, BF16)
+
+
 @pytest.mark.parametrize("N", [4, 200])
 def test_sharp_logits(gdr, N):
     """Logits up to some hundreds: all but one probability vanish, exponentials must not overflow."""
