@@ -43,25 +43,18 @@ struct GluEpi {
     int64_t M, F;
     int act;
     template <int MI, int NI>
-    __device__ __forceinline__ void operator()(const floatx4 (&acc)[2][MI][NI], int64_t m0, int64_t n0) const {
-        const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-        const bool wide = (F & 3) == 0;
+    __device__ __forceinline__ void operator()(const floatx4 (&acc)[2][MI][NI], int64_t m0, int64_t n0, int, char *st) const {
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-            const int64_t m = m0 + 16 * i + c;
-            if (m >= M) continue;
+            floatx4 v[NI];
 #pragma unroll
-            for (int j = 0; j < NI; ++j) {
-                const int64_t n = n0 + 16 * j + 4 * g;
-                if (n >= F) continue;
-                floatx4 v;
+            for (int j = 0; j < NI; ++j)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] = act_f(acc[0][i][j][r], act) * acc[1][i][j][r];
-                store4(h + m * F + n, v, F - n, wide);
-                if (gate) {
-                    store4(gate + m * F + n, acc[0][i][j], F - n, wide);
-                    store4(up + m * F + n, acc[1][i][j], F - n, wide);
-                }
+                for (int r = 0; r < 4; ++r) v[j][r] = act_f(acc[0][i][j][r], act) * acc[1][i][j][r];
+            store_rows<E, MI, NI>(st, v, h, F, m0 + 16 * i, n0, M, F);
+            if (gate) {
+                store_rows<E, MI, NI>(st, acc[0][i], gate, F, m0 + 16 * i, n0, M, F);
+                store_rows<E, MI, NI>(st, acc[1][i], up, F, m0 + 16 * i, n0, M, F);
             }
         }
     }
@@ -91,7 +84,7 @@ int64_t grad_ld(int64_t F) { return (F + 7) / 8 * 8; }
 
 template <typename E>
 hipError_t fwd_t(const FfnArgs &a, hipStream_t s) {
-    const GemmOp g{{a.x, nullptr}, {a.wg, a.wu}, a.D, a.D, a.M, a.F, a.D, 1};
+    const GemmOp g{{a.x, nullptr}, {a.wg, a.wu}, a.D, a.D, a.M, a.F, a.D};
     return launch_gemm<E, true, true, 2>(g, GluEpi<E>{(E *)a.h, (E *)a.gate, (E *)a.up, a.M, a.F, a.act}, s);
 }
 
@@ -106,16 +99,12 @@ hipError_t bwd_t(const FfnArgs &a, hipStream_t s) {
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         const GemmOp gx{{dg, du}, {a.wg, a.wu}, ld, a.D, a.M, a.D, a.F, 2};
-        e = launch_gemm<E, true, false, 1>(gx, StoreEpi<E>{(E *)a.dx, nullptr, nullptr, a.M, a.D, a.D}, s);
+        e = launch_gemm<E, true, false, 1>(gx, StoreEpi<E>{{(E *)a.dx, nullptr}, nullptr, nullptr, a.M, a.D, a.D}, s);
         if (e != hipSuccess) return e;
     }
-    for (int i = 0; i < 2; ++i) {
-        const GemmOp gw{{i ? du : dg, nullptr}, {a.x, nullptr}, ld, a.D, a.F, a.D, a.M, 1};
-        const hipError_t e =
-            launch_gemm<E, false, false, 1>(gw, StoreEpi<E>{(E *)(i ? a.dwu : a.dwg), nullptr, nullptr, a.F, a.D, a.D}, s);
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+    const GemmOp gw{{dg, du}, {a.x, a.x}, ld, a.D, a.F, a.D, a.M, 1, 2};
+    return launch_gemm<E, false, false, 1>(
+        gw, StoreEpi<E>{{(E *)a.dwg, (E *)a.dwu}, nullptr, nullptr, a.F, a.D, a.D}, s);
 }
 
 }  // namespace

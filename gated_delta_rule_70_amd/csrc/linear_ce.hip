@@ -13,6 +13,7 @@
 // dW's rows of the piece are complete and dx is summed over the pieces in 32 bits.
 #include <hip/hip_runtime.h>
 #include <math.h>
+#include <type_traits>
 #include <stdint.h>
 
 #include "gdr_kernels.hpp"
@@ -22,6 +23,10 @@
 namespace gdr {
 
 namespace {
+
+// The difference is taken before the change of base: at a logit equal to its reference the
+// exponential is 1 exactly.
+__device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
 
 // vocabulary columns per partial sum
 template <typename E>
@@ -35,27 +40,39 @@ struct StatEpi {
     float *tgt;    // [M]
     int64_t M, V;
     template <int MI, int NI>
-    __device__ __forceinline__ void operator()(const floatx4 (&acc)[1][MI][NI], int64_t m0, int64_t n0) const {
-        constexpr int SJ = NI < kTileCols / 16 ? NI : kTileCols / 16;  // tiles per strip
-        const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    __device__ __forceinline__ void operator()(const floatx4 (&acc)[1][MI][NI], int64_t m0, int64_t n0, int, char *st) const {
+        constexpr int SJ = NI < kTileCols / 16 ? NI : kTileCols / 16, S = NI / SJ;  // tiles per strip, strips
+        const int lane = epilogue_lane(), g = lane >> 4, c = lane & 15;
+        const int left = V - n0 < 16 * NI ? (int)(V - n0) : 16 * NI;  // columns in range
+        int want[MI];                                                 // the target's column among the wave's
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-            const int64_t m = m0 + 16 * i + c;
-            const int64_t tm = m < M ? t[m] : -1;
+            const int64_t m = m0 + 16 * i + c, n = (m < M ? t[m] : -1) - n0;
+            want[i] = n >= 0 && n < left ? (int)n : -1;
+        }
+        // The sums of every row first, without a branch (the accumulators stay where they are), then
+        // what a lane has to write.
+        float2 sums[MI][S];
+        float found[MI];
+        const int last = left - 4 * g;  // in-range columns of this lane: 16 j + r below it
+        auto reduce = [&](auto ragged) GDR_INLINE {
 #pragma unroll
-            for (int s = 0; s < NI / SJ; ++s) {
-                const int64_t ns = n0 + 16 * SJ * s;
-                if (ns >= V) continue;
-                const int left = V - ns < 16 * SJ ? (int)(V - ns) : 16 * SJ;        // columns in range
-                const int want = tm >= ns && tm < ns + left ? (int)(tm - ns) : -1;  // the target's column
+        for (int i = 0; i < MI; ++i) {
+            found[i] = 0.f;
+            const int at = want[i] - 4 * g;  // the target's 16 j + r, if this lane holds it
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                floatx4 v[SJ];
                 float top = -INFINITY, sum = 0.f;
 #pragma unroll
                 for (int j = 0; j < SJ; ++j)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int n = 16 * j + 4 * g + r;
-                        if (n < left) top = fmaxf(top, acc[0][i][SJ * s + j][r]);
-                        if (n == want) tgt[m] = acc[0][i][SJ * s + j][r];
+                        const int n = 16 * (SJ * s + j) + r;
+                        const float l = acc[0][i][SJ * s + j][r];
+                        found[i] = n == at ? l : found[i];
+                        v[j][r] = !ragged.value || n < last ? l : -INFINITY;
+                        top = fmaxf(top, v[j][r]);
                     }
                 top = fmaxf(top, __shfl_xor(top, 16, 64));
                 top = fmaxf(top, __shfl_xor(top, 32, 64));
@@ -63,12 +80,24 @@ struct StatEpi {
 #pragma unroll
                 for (int j = 0; j < SJ; ++j)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (16 * j + 4 * g + r < left) sum += __expf(acc[0][i][SJ * s + j][r] - ref);
+                    for (int r = 0; r < 4; ++r) sum += exp_f(v[j][r] - ref);
                 sum += __shfl_xor(sum, 16, 64);
                 sum += __shfl_xor(sum, 32, 64);
-                if (g == 0 && m < M) part[(ns / (16 * SJ)) * M + m] = make_float2(top, sum);
+                sums[i][s] = make_float2(top, sum);
+                __builtin_amdgcn_sched_barrier(0);  // one strip's values in registers at a time
             }
+        }
+        };
+        if (left == 16 * NI) reduce(std::false_type{});
+        else reduce(std::true_type{});
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const int64_t m = m0 + 16 * i + c;
+            // lane (g, c) holds columns 16 j + 4 g ..: the target's is among them where want / 4 % 4 == g
+            if (want[i] >= 0 && ((want[i] >> 2) & 3) == g) tgt[m] = found[i];
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                if (g == s % 4 && m < M && 16 * SJ * s < left) part[(n0 / (16 * SJ) + s) * M + m] = sums[i][s];
         }
     }
 };
@@ -81,50 +110,75 @@ struct GradEpi {
     E *dl;
     int64_t M, V, v0, width, ld;
     template <int MI, int NI>
-    __device__ __forceinline__ void operator()(const floatx4 (&acc)[1][MI][NI], int64_t m0, int64_t n0) const {
-        const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    __device__ __forceinline__ void operator()(const floatx4 (&acc)[1][MI][NI], int64_t m0, int64_t n0, int, char *st) const {
+        const int lane = epilogue_lane(), g = lane >> 4, c = lane & 15;
+        float ls[MI], sc[MI];
+        int want[MI], left[MI];  // the target's column and the piece's end, from this wave's first column
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             const int64_t m = m0 + 16 * i + c;
-            if (m >= M) continue;
-            const int64_t tm = t[m];
+            const int64_t tm = m < M ? t[m] : -1, tv = tm - v0 - n0;
             const bool on = tm >= 0 && tm < V;
-            const float ls = lse[m], sc = on ? dloss[m] : 0.f;
-            // the target's column and the piece's end, from this wave's first column
-            const int want = tm - v0 >= n0 && tm - v0 < n0 + 16 * NI ? (int)(tm - v0 - n0) : -1;
-            const int left = !on ? 0 : width - n0 < 16 * NI ? (int)(width - n0) : 16 * NI;
+            ls[i] = on ? lse[m] : 0.f;
+            sc[i] = on ? dloss[m] : 0.f;
+            want[i] = tv >= 0 && tv < 16 * NI ? (int)tv : -1;
+            left[i] = !on ? 0 : width - n0 < 16 * NI ? (int)(width - n0) : 16 * NI;
+        }
 #pragma unroll
-            for (int j = 0; j < NI; ++j) {
-                const int k = 16 * j + 4 * g;
-                const int64_t n = n0 + k;
-                if (n >= ld) continue;
-                floatx4 v;
+        for (int i = 0; i < MI; ++i) {
+            floatx4 v[NI];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float p = __expf(acc[0][i][j][r] - ls) - (k + r == want ? 1.f : 0.f);
-                    v[r] = k + r < left ? p * sc : 0.f;
-                }
-                store4(dl + m * ld + n, v, ld - n, true);
+            for (int j = 0; j < NI; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    v[j][r] = exp_f(acc[0][i][j][r] - ls[i]) * sc[i];
+            if (__any(want[i] >= 0)) {
+#pragma unroll
+                for (int j = 0; j < NI; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (16 * j + 4 * g + r == want[i])
+                            v[j][r] = (exp_f(acc[0][i][j][r] - ls[i]) - 1.f) * sc[i];
             }
+            if (__any(left[i] < 16 * NI)) {
+#pragma unroll
+                for (int j = 0; j < NI; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (16 * j + 4 * g + r >= left[i]) v[j][r] = 0.f;
+            }
+            store_rows<E, MI, NI>(st, v, dl, ld, m0 + 16 * i, n0, M, ld);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 };
 
-// one thread per token joins its partial sums in order
-__global__ __launch_bounds__(64) void ce_join_kernel(const float2 *part, const float *tgt, const int64_t *t, float *loss,
-                                                     float *lse, int64_t N, int64_t V, int64_t strips) {
-    const int64_t n = (int64_t)blockIdx.x * 64 + threadIdx.x;
-    if (n >= N) return;
-    float top = -INFINITY, sum = 0.f;
-    for (int64_t s = 0; s < strips; ++s) {
-        const float2 p = part[s * N + n];
-        const float m = fmaxf(top, p.x), ref = m == -INFINITY ? 0.f : m;
-        sum = sum * expf(top - ref) + p.y * expf(p.x - ref);
-        top = m;
+// Joins the partial sums of 16 tokens: 64 threads a token each take every 64th strip in order, then
+// the 64 are joined in pairs.
+__global__ __launch_bounds__(1024) void ce_join_kernel(const float2 *part, const float *tgt, const int64_t *t, float *loss,
+                                                       float *lse, int64_t N, int64_t V, int64_t strips) {
+    __shared__ float2 held[64][16];
+    const int c = threadIdx.x & 15, slot = threadIdx.x >> 4;
+    const int64_t n = (int64_t)blockIdx.x * 16 + c;
+    auto join = [](float2 p, float2 q) {
+        const float m = fmaxf(p.x, q.x), ref = m == -INFINITY ? 0.f : m;
+        return make_float2(m, p.y * expf(p.x - ref) + q.y * expf(q.x - ref));
+    };
+    float2 mine = make_float2(-INFINITY, 0.f);
+    if (n < N) {
+#pragma unroll 4
+        for (int64_t s = slot; s < strips; s += 64) mine = join(mine, part[s * N + n]);
     }
-    const float l = top + logf(sum);
-    lse[n] = l;
-    loss[n] = t[n] >= 0 && t[n] < V ? l - tgt[n] : 0.f;
+    held[slot][c] = mine;
+    for (int k = 32; k > 0; k >>= 1) {
+        __syncthreads();
+        if (slot < k) held[slot][c] = mine = join(mine, held[slot + k][c]);
+    }
+    if (slot == 0 && n < N) {
+        const float l = mine.x + logf(mine.y);
+        lse[n] = l;
+        loss[n] = t[n] >= 0 && t[n] < V ? l - tgt[n] : 0.f;
+    }
 }
 
 int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
@@ -147,10 +201,10 @@ hipError_t fwd_t(const CeArgs &a, hipStream_t s) {
     const int64_t strips = strips_of<E>(a.D, a.V);
     float *tgt = (float *)a.ws;
     float2 *part = (float2 *)((char *)a.ws + up256(a.N * 4));
-    const GemmOp g{{a.x, nullptr}, {a.w, nullptr}, a.D, a.D, a.N, a.V, a.D, 1};
+    const GemmOp g{{a.x, nullptr}, {a.w, nullptr}, a.D, a.D, a.N, a.V, a.D};
     const hipError_t e = launch_gemm<E, true, true, 1>(g, StatEpi{a.t, part, tgt, a.N, a.V}, s);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(ce_join_kernel, dim3((unsigned)((a.N + 63) / 64)), dim3(64), 0, s, part, tgt, a.t, a.loss, a.lse,
+    hipLaunchKernelGGL(ce_join_kernel, dim3((unsigned)((a.N + 15) / 16)), dim3(1024), 0, s, part, tgt, a.t, a.loss, a.lse,
                        a.N, a.V, strips);
     return hipGetLastError();
 }
@@ -163,17 +217,17 @@ hipError_t bwd_t(const CeArgs &a, hipStream_t s) {
     for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
         const int64_t width = a.V - v0 < piece ? a.V - v0 : piece;
         const E *w = (const E *)a.w + v0 * a.D;
-        const GemmOp gl{{a.x, nullptr}, {w, nullptr}, a.D, a.D, a.N, width, a.D, 1};
+        const GemmOp gl{{a.x, nullptr}, {w, nullptr}, a.D, a.D, a.N, width, a.D};
         hipError_t e = launch_gemm<E, true, true, 1>(
             gl, GradEpi<E>{a.t, a.lse_in, a.dloss, dl, a.N, a.V, v0, width, piece}, s);
         if (e != hipSuccess) return e;
-        const GemmOp gw{{dl, nullptr}, {a.x, nullptr}, piece, a.D, width, a.D, a.N, 1};
-        e = launch_gemm<E, false, false, 1>(gw, StoreEpi<E>{(E *)a.dw + v0 * a.D, nullptr, nullptr, width, a.D, a.D}, s);
+        const GemmOp gw{{dl, nullptr}, {a.x, nullptr}, piece, a.D, width, a.D, a.N};
+        e = launch_gemm<E, false, false, 1>(gw, StoreEpi<E>{{(E *)a.dw + v0 * a.D, nullptr}, nullptr, nullptr, width, a.D, a.D}, s);
         if (e != hipSuccess) return e;
         const bool last = v0 + piece >= a.V;
-        const GemmOp gx{{dl, nullptr}, {w, nullptr}, piece, a.D, a.N, a.D, width, 1};
+        const GemmOp gx{{dl, nullptr}, {w, nullptr}, piece, a.D, a.N, a.D, width};
         e = launch_gemm<E, true, false, 1>(
-            gx, StoreEpi<E>{last ? (E *)a.dx : nullptr, v0 ? acc : nullptr, acc, a.N, a.D, a.D}, s);
+            gx, StoreEpi<E>{{last ? (E *)a.dx : nullptr, nullptr}, v0 ? acc : nullptr, acc, a.N, a.D, a.D}, s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
