@@ -9,8 +9,22 @@
 //   dx = beta g,  db = beta (1 - beta) x g,  dla = alpha h_{t-1} g,  da = -e^{A_log} sigmoid(u) dla
 //   dA_log = sum dla la,  ddt_bias = sum da,  dh0 = alpha_1 g_1
 //
-// One thread per (sequence, channel) walks the tokens; neighbouring threads hold neighbouring
-// channels.
+// A step is the affine map h -> alpha h + beta x, and maps compose: (P, H) over several steps, P the
+// product of their alphas and H the end state from zero. A workgroup owns 16 V neighbouring channels
+// of a sequence (V = 2; 1 where D is odd) and walks it in blocks of 256 tokens: 32 time slots of 8
+// tokens side by side, 16 lanes of V channels each. A thread composes its 8 steps in registers, the
+// slots' maps are joined (shuffles within a wave, LDS between the eight waves, one barrier a
+// block), and the thread runs its steps again from the state that enters them: 8 more
+// multiply-adds, no second read. The next block's inputs are on their way meanwhile. The adjoint of
+// a block runs backwards with the same maps' products: (P, C) with C the gradient that leaves the
+// steps at their front; both directions' maps of a block are joined behind one barrier, the forward
+// one starting at the block's kept state.
+//
+// Memory is what bounds it: a read of x, a, b (and dout) and a write of the results, each once. Where
+// there are too few (sequence, channel tile) pairs for the 256 compute units the time axis is split
+// too: a first launch composes each chunk's map, and each workgroup of the second composes the
+// chunks before its own (behind it, in the backward) before it starts, at the cost of reading the
+// inputs of the maps twice.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -42,98 +56,477 @@ __device__ __forceinline__ Gates gates_of(float a, float b, float bias, float ra
     return g;
 }
 
-struct Span {
-    int64_t row0, len, slot0;
-    int step;  // +1, or -1 for a reversed scan (row0 is then the last row)
+constexpr int kThreads = 512, kWaves = kThreads / 64, kSlots = 4 * kWaves, kLen = kScanBlock / kSlots;
+static_assert(kLen * kSlots == kScanBlock, "block shape");
+
+// How a launch walks the sequences: whole, or in chunks of `chunk` tokens. Packed chunks of sequence
+// s begin at slot cu[s] / chunk + s.
+struct ScanPlan {
+    int64_t chunk;   // 0: not split
+    int64_t units;   // sequences, or chunk slots
+    int64_t ntile;   // channel tiles
+    int64_t per_seq; // chunks of a sequence (not packed)
 };
-__device__ __forceinline__ Span span_of(const ScanArgs &a, int64_t s) {
-    Span p;
+
+// One unit: tokens [t0, t1) of a sequence in scan order.
+struct Unit {
+    int64_t s, row0, len, slot0;  // sequence, its first row, its tokens, its first block slot
+    int64_t c, base, t0, t1;      // the chunk and the unit index of the sequence's first chunk
+    bool last;                    // the sequence ends with this unit
+};
+__device__ __forceinline__ Unit unit_of(const ScanArgs &a, const ScanPlan &p, int64_t u) {
+    Unit n;
+    n.s = u;
+    n.c = 0;
+    n.base = u;
+    if (p.chunk) {
+        if (a.cu_seqlens) {  // the last sequence whose first chunk is at or before u
+            int64_t lo = 0, hi = a.nseq - 1;
+            while (lo < hi) {
+                const int64_t mid = (lo + hi + 1) / 2;
+                if (a.cu_seqlens[mid] / p.chunk + mid <= u) lo = mid;
+                else hi = mid - 1;
+            }
+            n.s = lo;
+            n.base = a.cu_seqlens[lo] / p.chunk + lo;
+        } else {
+            n.s = u / p.per_seq;
+            n.base = n.s * p.per_seq;
+        }
+        n.c = u - n.base;
+    }
     if (a.cu_seqlens) {
-        const int64_t c0 = a.cu_seqlens[s];
-        p.row0 = c0;
-        p.len = a.cu_seqlens[s + 1] - c0;
-        p.slot0 = c0 / kScanBlock + s;
+        n.row0 = a.cu_seqlens[n.s];
+        n.len = a.cu_seqlens[n.s + 1] - n.row0;
+        n.slot0 = n.row0 / kScanBlock + n.s;
     } else {
-        p.row0 = s * a.T;
-        p.len = a.T;
-        p.slot0 = s * ((a.T + kScanBlock - 1) / kScanBlock);
+        n.row0 = n.s * a.T;
+        n.len = a.T;
+        n.slot0 = n.s * ((a.T + kScanBlock - 1) / kScanBlock);
     }
-    p.step = 1;
-    if (a.flags & kFlagReverse) {
-        p.row0 += p.len - 1;
-        p.step = -1;
-    }
-    return p;
+    n.t0 = p.chunk ? n.c * p.chunk : 0;
+    n.t1 = p.chunk && n.t0 + p.chunk < n.len ? n.t0 + p.chunk : n.len;
+    n.last = n.t1 == n.len && (n.t0 < n.len || n.c == 0);
+    return n;
 }
 
-template <typename E>
-__global__ __launch_bounds__(64) void scan_fwd_kernel(ScanArgs a, int64_t ntile) {
-    const int64_t s = blockIdx.x / ntile, d = (blockIdx.x % ntile) * 64 + threadIdx.x;
-    if (d >= a.D) return;
-    const Span p = span_of(a, s);
-    const E *x = (const E *)a.x, *ra = (const E *)a.a, *rb = (const E *)a.b;
-    E *out = (E *)a.out;
-    const float rate = expf(a.A_log[d]), bias = a.dt_bias[d];
-    float h = a.h0 ? a.h0[s * a.D + d] : 0.f;
-    for (int64_t t = 0; t < p.len; ++t) {
-        if (a.states && t % kScanBlock == 0) a.states[(p.slot0 + t / kScanBlock) * a.D + d] = h;
-        const int64_t i = (p.row0 + p.step * t) * a.D + d;
-        const Gates g = gates_of((float)ra[i], (float)rb[i], bias, rate);
-        h = g.alpha * h + g.beta * (float)x[i];
-        out[i] = (E)h;
-    }
-    if (a.hT) a.hT[s * a.D + d] = h;
-}
+// What a thread is: V channels from d0, slot `slot` of the block.
+template <typename E, int V>
+struct Lane {
+    typedef E Raw __attribute__((ext_vector_type(V)));
+    int wave, sub, col, slot;
+    int64_t d0;
+    bool on;                 // its channels exist
+    unsigned off[kLen];      // bytes from a block's first row (in memory) to its tokens' channels
+    unsigned safe;           // ... to an address that any block with a token has
 
-template <typename E>
-__global__ __launch_bounds__(64) void scan_bwd_kernel(ScanArgs a, int64_t ntile) {
-    __shared__ float hbuf[kScanBlock][64];
-    const int64_t s = blockIdx.x / ntile, d = (blockIdx.x % ntile) * 64 + threadIdx.x;
-    if (d >= a.D) return;
-    const Span p = span_of(a, s);
-    const E *x = (const E *)a.x, *ra = (const E *)a.a, *rb = (const E *)a.b, *dout = (const E *)a.dout;
-    E *dx = (E *)a.dx, *da = (E *)a.da, *db = (E *)a.db;
-    const float rate = expf(a.A_log[d]), bias = a.dt_bias[d];
-    float g = a.dhT ? a.dhT[s * a.D + d] : 0.f, sA = 0.f, sb = 0.f;
-    const int64_t nb = (p.len + kScanBlock - 1) / kScanBlock;
-    for (int64_t k = nb - 1; k >= 0; --k) {
-        const int n = (int)(p.len - k * kScanBlock < kScanBlock ? p.len - k * kScanBlock : kScanBlock);
-        float h = a.states[(p.slot0 + k) * a.D + d];
-        for (int t = 0; t < n; ++t) {
-            const int64_t i = (p.row0 + p.step * (k * kScanBlock + t)) * a.D + d;
-            const Gates q = gates_of((float)ra[i], (float)rb[i], bias, rate);
-            hbuf[t][threadIdx.x] = h;
-            h = q.alpha * h + q.beta * (float)x[i];
+    __device__ __forceinline__ void init(const ScanArgs &a, int64_t tile) {
+        const int lane = threadIdx.x & 63;
+        wave = threadIdx.x >> 6;
+        sub = lane >> 4;
+        col = lane & 15;
+        slot = 4 * wave + sub;
+        d0 = (tile * 16 + col) * V;
+        on = d0 < a.D;
+        const bool rev = a.flags & kFlagReverse;
+        const unsigned pitch = (unsigned)(a.D * sizeof(E));
+#pragma unroll
+        for (int j = 0; j < kLen; ++j) {
+            const int t = slot * kLen + j;
+            off[j] = (rev ? kScanBlock - 1 - t : t) * pitch + (unsigned)(d0 * sizeof(E));
         }
-        for (int t = n - 1; t >= 0; --t) {
-            const int64_t i = (p.row0 + p.step * (k * kScanBlock + t)) * a.D + d;
-            const Gates q = gates_of((float)ra[i], (float)rb[i], bias, rate);
-            g += (float)dout[i];
-            const float dla = q.alpha * hbuf[t][threadIdx.x] * g, dai = -q.rs * dla;
-            dx[i] = (E)(q.beta * g);
-            db[i] = (E)(q.beta * (1.f - q.beta) * (float)x[i] * g);
-            da[i] = (E)dai;
-            sA += dla * q.la;
-            sb += dai;
-            g *= q.alpha;
-        }
+        safe = rev ? (kScanBlock - 1) * pitch : 0;
     }
-    if (a.dh0) a.dh0[s * a.D + d] = g;
-    a.ws[(2 * s) * a.D + d] = sA;
-    a.ws[(2 * s + 1) * a.D + d] = sb;
+    // whether token j of the thread's slot is among the first n of the block
+    __device__ __forceinline__ bool has(int j, int n) const { return on && slot * kLen + j < n; }
+    __device__ __forceinline__ void load(Raw (&r)[kLen], const E *p, int n) const {
+#pragma unroll
+        for (int j = 0; j < kLen; ++j)
+            r[j] = *reinterpret_cast<const Raw *>(reinterpret_cast<const char *>(p) + (has(j, n) ? off[j] : safe));
+    }
+    __device__ __forceinline__ void store(E *p, int j, const float (&v)[V]) const {
+        Raw r;
+#pragma unroll
+        for (int i = 0; i < V; ++i) r[i] = (E)v[i];
+        *reinterpret_cast<Raw *>(reinterpret_cast<char *>(p) + off[j]) = r;
+    }
+};
+
+// The first row, in memory, of the block that begins at token t of unit n's sequence.
+__device__ __forceinline__ int64_t block_row(const ScanArgs &a, const Unit &n, int64_t t) {
+    return a.flags & kFlagReverse ? n.row0 + n.len - t - kScanBlock : n.row0 + t;
 }
 
-// dA_log and ddt_bias: the partial sums [n][2][D] added in order
-__global__ __launch_bounds__(64) void scan_param_kernel(const float *ws, int64_t n, int64_t D, float *dA, float *db) {
-    const int64_t d = (int64_t)blockIdx.x * 64 + threadIdx.x;
-    if (d >= D) return;
+// Joins the slots' maps (P, H) in time order. `in` becomes the state entering the thread's slot
+// when `carry` enters the block, `carry` the state that leaves the block, `whole` (the product of
+// all alphas so far) is multiplied on. BACK joins from the last slot to the first.
+template <int V>
+struct WaveMap {
+    float P[V], H[V];
+};
+template <int V, bool BACK>
+__device__ __forceinline__ void join_in_wave(int sub, const float (&P)[V], const float (&H)[V], WaveMap<V> &all, WaveMap<V> &before) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float p = P[i], h = H[i];
+#pragma unroll
+        for (int d = 1; d < 4; d *= 2) {
+            const float q = BACK ? __shfl_down(p, 16 * d, 64) : __shfl_up(p, 16 * d, 64);
+            const float g = BACK ? __shfl_down(h, 16 * d, 64) : __shfl_up(h, 16 * d, 64);
+            if (BACK ? sub + d < 4 : sub >= d) {
+                h = fmaf(p, g, h);
+                p *= q;
+            }
+        }
+        all.P[i] = p;
+        all.H[i] = h;
+        const float q = BACK ? __shfl_down(p, 16, 64) : __shfl_up(p, 16, 64);
+        const float g = BACK ? __shfl_down(h, 16, 64) : __shfl_up(h, 16, 64);
+        const bool first = BACK ? sub == 3 : sub == 0;
+        before.P[i] = first ? 1.f : q;
+        before.H[i] = first ? 0.f : g;
+    }
+}
+template <int V, bool BACK>
+__device__ __forceinline__ void join_waves(const WaveMap<V> (*rec)[16], int wave, int col, const WaveMap<V> &before,
+                                           float (&carry)[V], float (&whole)[V], float (&in)[V]) {
+    float mine[V];
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) {
+        const int w = BACK ? kWaves - 1 - k : k;
+        const WaveMap<V> m = rec[w][col];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (w == wave) mine[i] = carry[i];
+            carry[i] = fmaf(m.P[i], carry[i], m.H[i]);
+            whole[i] *= m.P[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) in[i] = fmaf(before.P[i], mine[i], before.H[i]);
+}
+
+// The state entering chunk n.c of a sequence (BACK: the gradient entering it from behind): the maps of
+// the chunks before it (behind it), composed by the 32 slots side by side and then joined.
+template <int V, bool BACK>
+__device__ __forceinline__ void fold_chunks(const ScanArgs &a, const Unit &n, const ScanPlan &p, const float2 *agg, int slot, int sub,
+                                            int wave, int col, int64_t d0, bool on, WaveMap<V> (*rec)[16], float (&carry)[V]) {
+    const int64_t chunks = (n.len + p.chunk - 1) / p.chunk;
+    const int64_t first = BACK ? n.c + 1 : 0, count = BACK ? chunks - first : n.c;
+    float P[V], H[V], in[V], whole[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        P[i] = whole[i] = 1.f;
+        H[i] = 0.f;
+    }
+    const int64_t lo = first + count * slot / kSlots, hi = first + count * (slot + 1) / kSlots;
+    if (on)
+        for (int64_t k = lo; k < hi; ++k) {
+            const int64_t c = BACK ? lo + hi - 1 - k : k;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float2 m = agg[(n.base + c) * a.D + d0 + i];
+                if (!BACK && c == 0) m.x = 0.f;  // holds the initial state, see scan_fwd_kernel
+                H[i] = fmaf(m.x, H[i], m.y);
+                P[i] *= m.x;
+            }
+        }
+    WaveMap<V> all, before;
+    join_in_wave<V, BACK>(sub, P, H, all, before);
+    if (sub == (BACK ? 0 : 3)) rec[wave][col] = all;
+    __syncthreads();
+    join_waves<V, BACK>(rec, wave, col, before, carry, whole, in);
+}
+
+enum ScanMode { kWhole, kCompose, kApply };
+
+// workgroup -> (unit, channel tile), the tiles of a unit side by side on one XCD: their rows share
+// 128-byte lines
+__device__ __forceinline__ int64_t xcd_order(int64_t all) {
+    const int64_t id = blockIdx.x, x = id & 7, q = all >> 3, r = all & 7;
+    return x * q + (x < r ? x : r) + (id >> 3);
+}
+
+template <typename E, int V, int MODE>
+__global__ __launch_bounds__(kThreads, 2) void scan_fwd_kernel(ScanArgs a, ScanPlan p, float2 *agg) {
+    __shared__ WaveMap<V> rec[2][kWaves][16];
+    const int64_t w = xcd_order(p.units * p.ntile), u = w / p.ntile;
+    const Unit n = unit_of(a, p, u);
+    if (p.chunk && n.t0 >= n.len && n.c > 0) return;  // a slot without a chunk
+    Lane<E, V> ln;
+    ln.init(a, w % p.ntile);
+    typedef typename Lane<E, V>::Raw Raw;
+
+    float rate[V], bias[V], carry[V], whole[V], initial[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int64_t d = ln.on ? ln.d0 + i : 0;
+        rate[i] = expf(a.A_log[d]);
+        bias[i] = a.dt_bias[d];
+        // Split: the first launch takes the initial state into the first chunk's map and keeps a copy of
+        // it where that map's product would stand; the second does not read h0, which its last chunk
+        // may overwrite (hT in place).
+        if (MODE == kApply) carry[i] = n.c == 0 && ln.on ? agg[u * a.D + d].x : 0.f;
+        else carry[i] = n.c == 0 && a.h0 && ln.on ? a.h0[n.s * a.D + d] : 0.f;
+        whole[i] = 1.f;
+        initial[i] = carry[i];
+    }
+    if (MODE == kApply) {
+        fold_chunks<V, false>(a, n, p, agg, ln.slot, ln.sub, ln.wave, ln.col, ln.d0, ln.on, rec[1], carry);
+    }
+
+    Raw rx[kLen], ra[kLen], rb[kLen];
+    auto fetch = [&](int64_t t) __attribute__((always_inline)) {
+        const int64_t row = block_row(a, n, t) * a.D;
+        const int left = n.t1 - t < kScanBlock ? (int)(n.t1 - t) : kScanBlock;
+        ln.load(rx, (const E *)a.x + row, left);
+        ln.load(ra, (const E *)a.a + row, left);
+        ln.load(rb, (const E *)a.b + row, left);
+    };
+    if (n.t0 < n.t1) fetch(n.t0);
+    int buf = 0;
+    for (int64_t t = n.t0; t < n.t1; t += kScanBlock, buf ^= 1) {
+        const int left = n.t1 - t < kScanBlock ? (int)(n.t1 - t) : kScanBlock;
+        Raw x[kLen], ga[kLen], gb[kLen];
+#pragma unroll
+        for (int j = 0; j < kLen; ++j) {
+            x[j] = rx[j];
+            ga[j] = ra[j];
+            gb[j] = rb[j];
+        }
+        if (t + kScanBlock < n.t1) fetch(t + kScanBlock);
+        if (MODE != kCompose && a.states && ln.slot == 0 && ln.on) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) a.states[(n.slot0 + t / kScanBlock) * a.D + ln.d0 + i] = carry[i];
+        }
+        float al[kLen][V], v[kLen][V], P[V], H[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            P[i] = 1.f;
+            H[i] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kLen; ++j) {
+            const bool in = left == kScanBlock || ln.has(j, left);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const Gates g = gates_of((float)ga[j][i], (float)gb[j][i], bias[i], rate[i]);
+                al[j][i] = in ? g.alpha : 1.f;
+                v[j][i] = in ? g.beta * (float)x[j][i] : 0.f;
+                H[i] = fmaf(al[j][i], H[i], v[j][i]);
+                P[i] *= al[j][i];
+            }
+        }
+        WaveMap<V> all, before;
+        join_in_wave<V, false>(ln.sub, P, H, all, before);
+        if (ln.sub == 3) rec[buf][ln.wave][ln.col] = all;
+        __syncthreads();
+        float h[V];
+        join_waves<V, false>(rec[buf], ln.wave, ln.col, before, carry, whole, h);
+        if (MODE == kCompose) continue;
+        E *out = (E *)a.out + block_row(a, n, t) * a.D;
+#pragma unroll
+        for (int j = 0; j < kLen; ++j) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) h[i] = fmaf(al[j][i], h[i], v[j][i]);
+            if (ln.has(j, left)) ln.store(out, j, h);
+        }
+    }
+    if (ln.slot == 0 && ln.on) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (MODE == kCompose) agg[u * a.D + ln.d0 + i] = make_float2(n.c == 0 ? initial[i] : whole[i], carry[i]);
+            else if (a.hT && n.last) a.hT[n.s * a.D + ln.d0 + i] = carry[i];
+        }
+    }
+}
+
+// MODE kCompose: the maps (P, C) of the chunks' adjoints, which need a and dout alone.
+template <typename E, int V, int MODE>
+__global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, ScanPlan p, float2 *agg, float *sums) {
+    __shared__ WaveMap<V> rec[2][kWaves][16], rec_back[2][kWaves][16];
+    __shared__ float part[2][V][kSlots][16];
+    const int64_t w = xcd_order(p.units * p.ntile), u = w / p.ntile;
+    const Unit n = unit_of(a, p, u);
+    Lane<E, V> ln;
+    ln.init(a, w % p.ntile);
+    const bool none = p.chunk && n.t0 >= n.len && n.c > 0;  // a slot without a chunk
+    if (none) {
+        if (MODE != kCompose && ln.slot == 0 && ln.on)
+#pragma unroll
+            for (int i = 0; i < V; ++i) sums[2 * u * a.D + ln.d0 + i] = sums[(2 * u + 1) * a.D + ln.d0 + i] = 0.f;
+        return;
+    }
+    typedef typename Lane<E, V>::Raw Raw;
+
+    float rate[V], bias[V], carry[V], whole[V], sA[V], sb[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int64_t d = ln.on ? ln.d0 + i : 0;
+        rate[i] = expf(a.A_log[d]);
+        bias[i] = a.dt_bias[d];
+        carry[i] = MODE != kCompose && a.dhT && ln.on ? a.dhT[n.s * a.D + d] : 0.f;
+        whole[i] = 1.f;
+        sA[i] = sb[i] = 0.f;
+    }
+    if (MODE == kApply) {
+        fold_chunks<V, true>(a, n, p, agg, ln.slot, ln.sub, ln.wave, ln.col, ln.d0, ln.on, rec_back[1], carry);
+        __syncthreads();
+    }
+
+    Raw rx[kLen], ra[kLen], rb[kLen], rg[kLen];
+    auto fetch = [&](int64_t t) __attribute__((always_inline)) {
+        const int64_t row = block_row(a, n, t) * a.D;
+        const int left = n.t1 - t < kScanBlock ? (int)(n.t1 - t) : kScanBlock;
+        ln.load(ra, (const E *)a.a + row, left);
+        ln.load(rg, (const E *)a.dout + row, left);
+        if (MODE != kCompose) {
+            ln.load(rx, (const E *)a.x + row, left);
+            ln.load(rb, (const E *)a.b + row, left);
+        }
+    };
+    const int64_t blocks = (n.t1 - n.t0 + kScanBlock - 1) / kScanBlock;
+    if (blocks > 0) fetch(n.t0 + (blocks - 1) * kScanBlock);
+    int buf = 0;
+    for (int64_t k = blocks - 1; k >= 0; --k, buf ^= 1) {
+        const int64_t t = n.t0 + k * kScanBlock;
+        const int left = n.t1 - t < kScanBlock ? (int)(n.t1 - t) : kScanBlock;
+        Raw x[kLen], ga[kLen], gb[kLen], go[kLen];
+#pragma unroll
+        for (int j = 0; j < kLen; ++j) {
+            x[j] = rx[j];
+            ga[j] = ra[j];
+            gb[j] = rb[j];
+            go[j] = rg[j];
+        }
+        float start[V];
+        if (MODE != kCompose) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) start[i] = a.states[(n.slot0 + t / kScanBlock) * a.D + (ln.on ? ln.d0 + i : 0)];
+        }
+        if (k > 0) fetch(t - kScanBlock);
+        Gates q[kLen][V];
+        float P[V], H[V], C[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            P[i] = 1.f;
+            H[i] = C[i] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kLen; ++j) {
+            const bool in = left == kScanBlock || ln.has(j, left);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                Gates g = gates_of((float)ga[j][i], MODE == kCompose ? 0.f : (float)gb[j][i], bias[i], rate[i]);
+                if (!in) {  // past the end: the identity, with no gradient of its own
+                    g.alpha = 1.f;
+                    g.beta = g.la = g.rs = 0.f;
+                    go[j][i] = (E)0.f;
+                }
+                q[j][i] = g;
+                if (MODE != kCompose) H[i] = fmaf(g.alpha, H[i], g.beta * (float)x[j][i]);
+                P[i] *= g.alpha;
+            }
+        }
+#pragma unroll
+        for (int j = kLen - 1; j >= 0; --j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) C[i] = q[j][i].alpha * ((float)go[j][i] + C[i]);
+        WaveMap<V> all, before, all_back, before_back;
+        join_in_wave<V, true>(ln.sub, P, C, all_back, before_back);
+        if (ln.sub == 0) rec_back[buf][ln.wave][ln.col] = all_back;
+        if (MODE != kCompose) {
+            join_in_wave<V, false>(ln.sub, P, H, all, before);
+            if (ln.sub == 3) rec[buf][ln.wave][ln.col] = all;
+        }
+        __syncthreads();
+        float c[V];
+        join_waves<V, true>(rec_back[buf], ln.wave, ln.col, before_back, carry, whole, c);
+        if (MODE == kCompose) continue;
+        float h[V], prev[kLen][V], unused[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) unused[i] = 1.f;
+        join_waves<V, false>(rec[buf], ln.wave, ln.col, before, start, unused, h);
+#pragma unroll
+        for (int j = 0; j < kLen; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                prev[j][i] = h[i];
+                h[i] = fmaf(q[j][i].alpha, h[i], q[j][i].beta * (float)x[j][i]);
+            }
+        const int64_t row = block_row(a, n, t) * a.D;
+        E *dx = (E *)a.dx + row, *da = (E *)a.da + row, *db = (E *)a.db + row;
+#pragma unroll
+        for (int j = kLen - 1; j >= 0; --j) {
+            float vx[V], va[V], vb[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const Gates &g = q[j][i];
+                const float up = (float)go[j][i] + c[i];
+                const float dla = g.alpha * prev[j][i] * up;
+                vx[i] = g.beta * up;
+                va[i] = -g.rs * dla;
+                vb[i] = vx[i] * (1.f - g.beta) * (float)x[j][i];
+                sA[i] = fmaf(dla, g.la, sA[i]);
+                sb[i] += va[i];
+                c[i] = g.alpha * up;
+            }
+            if (ln.has(j, left)) {
+                ln.store(dx, j, vx);
+                ln.store(da, j, va);
+                ln.store(db, j, vb);
+            }
+        }
+    }
+    if (MODE == kCompose) {
+        if (ln.slot == 0 && ln.on)
+#pragma unroll
+            for (int i = 0; i < V; ++i) agg[u * a.D + ln.d0 + i] = make_float2(whole[i], carry[i]);
+        return;
+    }
+    // the parameters' sums of this unit: the slots' in order
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        part[0][i][ln.slot][ln.col] = sA[i];
+        part[1][i][ln.slot][ln.col] = sb[i];
+    }
+    __syncthreads();
+    if (ln.slot < 2 && ln.on) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float s = 0.f;
+#pragma unroll
+            for (int k = 0; k < kSlots; ++k) s += part[ln.slot][i][k][ln.col];
+            sums[(2 * u + ln.slot) * a.D + ln.d0 + i] = s;
+        }
+    }
+    if (ln.slot == 0 && ln.on && a.dh0 && n.c == 0) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) a.dh0[n.s * a.D + ln.d0 + i] = carry[i];
+    }
+}
+
+// dA_log and ddt_bias: the units' sums [units][2][D], 16 slices of the units side by side and then
+// in order
+__global__ __launch_bounds__(1024) void scan_param_kernel(const float *sums, int64_t units, int64_t D, float *dA, float *db) {
+    __shared__ float held[2][16][64];
+    const int lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
+    const int64_t d = (int64_t)blockIdx.x * 64 + lane;
     float sA = 0.f, sb = 0.f;
-    for (int64_t i = 0; i < n; ++i) {
-        sA += ws[2 * i * D + d];
-        sb += ws[(2 * i + 1) * D + d];
+    if (d < D)
+        for (int64_t i = units * slice / 16; i < units * (slice + 1) / 16; ++i) {
+            sA += sums[2 * i * D + d];
+            sb += sums[(2 * i + 1) * D + d];
+        }
+    held[0][slice][lane] = sA;
+    held[1][slice][lane] = sb;
+    __syncthreads();
+    if (slice < 2 && d < D) {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) s += held[slice][k][lane];
+        (slice ? db : dA)[d] = s;
     }
-    dA[d] = sA;
-    db[d] = sb;
 }
 
 template <typename E>
@@ -147,31 +540,87 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a) {
     ((E *)a.out)[i] = (E)h;
 }
 
-}  // namespace
+int vec_of(int64_t D) { return D % 2 ? 1 : 2; }
 
-int64_t scan_fwd_ws_bytes(int64_t, int64_t, int64_t) { return 0; }
-int64_t scan_bwd_ws_bytes(int64_t D, int64_t nseq, int64_t) { return nseq * D * 8; }
+// Split where whole sequences would leave compute units idle: fewer than 224 workgroups (of 256), or,
+// packed, fewer than 1024 (their lengths differ and are not known here). Chunks are whole blocks, of a
+// size that gives about 768 workgroups: three a compute unit, which evens out the ends.
+ScanPlan plan_of(int64_t T, int64_t D, int64_t nseq, bool packed) {
+    ScanPlan p;
+    const int64_t cols = 16 * vec_of(D);
+    p.ntile = (D + cols - 1) / cols;
+    p.chunk = 0;
+    p.units = nseq;
+    p.per_seq = 1;
+    const int64_t rows = packed ? T : nseq * T, blocks = (rows + kScanBlock - 1) / kScanBlock;
+    if (T <= kScanBlock || nseq * p.ntile >= (packed ? 1024 : 224)) return p;
+    const int64_t per = (blocks * p.ntile + 767) / 768;
+    p.chunk = per * kScanBlock;
+    p.per_seq = (T + p.chunk - 1) / p.chunk;
+    p.units = packed ? T / p.chunk + nseq + 1 : nseq * p.per_seq;
+    return p;
+}
+ScanPlan plan_of(const ScanArgs &a) { return plan_of(a.T, a.D, a.nseq, a.cu_seqlens != nullptr); }
 
-hipError_t launch_scan_fwd(const ScanArgs &a, int dtype, hipStream_t s) {
-    const int64_t ntile = (a.D + 63) / 64;
-    if (a.nseq == 0) return hipSuccess;
-    const dim3 grid((unsigned)(ntile * a.nseq)), block(64);
-    if (dtype == kDtypeBf16) hipLaunchKernelGGL((scan_fwd_kernel<__bf16>), grid, block, 0, s, a, ntile);
-    else hipLaunchKernelGGL((scan_fwd_kernel<float>), grid, block, 0, s, a, ntile);
+template <typename E, int V>
+hipError_t fwd_t(const ScanArgs &a, hipStream_t s) {
+    const ScanPlan p = plan_of(a);
+    const dim3 grid((unsigned)(p.units * p.ntile)), block(kThreads);
+    float2 *agg = (float2 *)a.ws;
+    if (!p.chunk) {
+        hipLaunchKernelGGL((scan_fwd_kernel<E, V, kWhole>), grid, block, 0, s, a, p, agg);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL((scan_fwd_kernel<E, V, kCompose>), grid, block, 0, s, a, p, agg);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((scan_fwd_kernel<E, V, kApply>), grid, block, 0, s, a, p, agg);
     return hipGetLastError();
 }
 
-hipError_t launch_scan_bwd(const ScanArgs &a, int dtype, hipStream_t s) {
-    const int64_t ntile = (a.D + 63) / 64;
+template <typename E, int V>
+hipError_t bwd_t(const ScanArgs &a, hipStream_t s) {
+    const ScanPlan p = plan_of(a);
+    const dim3 grid((unsigned)(p.units * p.ntile)), block(kThreads);
+    float *sums = a.ws;
+    float2 *agg = (float2 *)(a.ws + 2 * p.units * a.D);
     if (a.nseq > 0) {
-        const dim3 grid((unsigned)(ntile * a.nseq)), block(64);
-        if (dtype == kDtypeBf16) hipLaunchKernelGGL((scan_bwd_kernel<__bf16>), grid, block, 0, s, a, ntile);
-        else hipLaunchKernelGGL((scan_bwd_kernel<float>), grid, block, 0, s, a, ntile);
+        if (p.chunk) {
+            hipLaunchKernelGGL((scan_bwd_kernel<E, V, kCompose>), grid, block, 0, s, a, p, agg, sums);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            hipLaunchKernelGGL((scan_bwd_kernel<E, V, kApply>), grid, block, 0, s, a, p, agg, sums);
+        } else {
+            hipLaunchKernelGGL((scan_bwd_kernel<E, V, kWhole>), grid, block, 0, s, a, p, agg, sums);
+        }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(scan_param_kernel, dim3((unsigned)ntile), dim3(64), 0, s, a.ws, a.nseq, a.D, a.dA_log, a.ddt_bias);
+    hipLaunchKernelGGL(scan_param_kernel, dim3((unsigned)((a.D + 63) / 64)), dim3(1024), 0, s, sums, a.nseq ? p.units : 0, a.D,
+                       a.dA_log, a.ddt_bias);
     return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t scan_fwd_ws_bytes(int64_t T, int64_t D, int64_t nseq, bool packed) {
+    const ScanPlan p = plan_of(T, D, nseq, packed);
+    return p.chunk ? p.units * D * 8 : 0;
+}
+int64_t scan_bwd_ws_bytes(int64_t T, int64_t D, int64_t nseq, bool packed) {
+    const ScanPlan p = plan_of(T, D, nseq, packed);
+    return p.units * D * (p.chunk ? 16 : 8);
+}
+
+hipError_t launch_scan_fwd(const ScanArgs &a, int dtype, hipStream_t s) {
+    if (a.nseq == 0) return hipSuccess;
+    if (dtype == kDtypeBf16) return vec_of(a.D) == 2 ? fwd_t<__bf16, 2>(a, s) : fwd_t<__bf16, 1>(a, s);
+    return vec_of(a.D) == 2 ? fwd_t<float, 2>(a, s) : fwd_t<float, 1>(a, s);
+}
+
+hipError_t launch_scan_bwd(const ScanArgs &a, int dtype, hipStream_t s) {
+    if (dtype == kDtypeBf16) return vec_of(a.D) == 2 ? bwd_t<__bf16, 2>(a, s) : bwd_t<__bf16, 1>(a, s);
+    return vec_of(a.D) == 2 ? bwd_t<float, 2>(a, s) : bwd_t<float, 1>(a, s);
 }
 
 hipError_t launch_scan_step(const ScanArgs &a, int dtype, hipStream_t s) {

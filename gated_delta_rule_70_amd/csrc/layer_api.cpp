@@ -64,6 +64,9 @@ gdr_status_t launched(hipError_t e, const char *what) {
     return GDR_OK;
 }
 
+// rows are walked with 32-bit offsets within a tile or a block of tokens
+constexpr int64_t kMaxWidth = INT64_C(1) << 20;
+
 // ------------------------------------------------------------------ channel scan
 
 struct ScanSizes {
@@ -76,8 +79,8 @@ gdr_status_t scan_sizes(const gdr_scan_dims_t *dims, bool packed, ScanSizes *z) 
     const gdr_status_t s = check_dtype(d.dtype);
     if (s != GDR_OK) return s;
     if (d.flags & ~GDR_REVERSE) return fail(GDR_ERR_FLAGS, "flags 0x%x: the channel scan takes GDR_REVERSE only", d.flags);
-    if (d.B < 0 || d.T < 0 || d.D < 1)
-        return fail(GDR_ERR_DIMS, "B (%lld) and T (%lld) must be >= 0 and D (%lld) >= 1", (long long)d.B, (long long)d.T, (long long)d.D);
+    if (d.B < 0 || d.T < 0 || d.D < 1 || d.D > kMaxWidth)
+        return fail(GDR_ERR_DIMS, "B (%lld) and T (%lld) must be >= 0 and D (%lld) in [1, 2^20]", (long long)d.B, (long long)d.T, (long long)d.D);
     if (d.T > INT32_MAX) return fail(GDR_ERR_DIMS, "T must be below 2^31");
     z->nseq = d.B;
     if (packed) {
@@ -117,9 +120,6 @@ gdr_status_t check_workspace(const void *ws, int64_t have, int64_t need) {
 }
 
 // ------------------------------------------------------------------ feed-forward and cross entropy
-
-// rows of one operand are walked with 32-bit offsets within a tile
-constexpr int64_t kMaxWidth = INT64_C(1) << 20;
 
 gdr_status_t ffn_sizes(const gdr_ffn_dims_t *dims) {
     if (!dims) return fail(GDR_ERR_NULL, "dims is NULL");
@@ -162,13 +162,13 @@ int64_t gdr_channel_scan_states_elems(const gdr_scan_dims_t *dims, int32_t packe
 int64_t gdr_channel_scan_fwd_workspace_bytes(const gdr_scan_dims_t *dims, int32_t packed) {
     ScanSizes z;
     if (scan_sizes(dims, packed != 0, &z) != GDR_OK) return -1;
-    return gdr::scan_fwd_ws_bytes(dims->D, z.nseq, z.slots);
+    return gdr::scan_fwd_ws_bytes(dims->T, dims->D, z.nseq, packed != 0);
 }
 
 int64_t gdr_channel_scan_bwd_workspace_bytes(const gdr_scan_dims_t *dims, int32_t packed) {
     ScanSizes z;
     if (scan_sizes(dims, packed != 0, &z) != GDR_OK) return -1;
-    return gdr::scan_bwd_ws_bytes(dims->D, z.nseq, z.slots);
+    return gdr::scan_bwd_ws_bytes(dims->T, dims->D, z.nseq, packed != 0);
 }
 
 gdr_status_t gdr_channel_scan_fwd(const void *x, const void *a, const void *b, const float *A_log, const float *dt_bias,
@@ -179,7 +179,7 @@ gdr_status_t gdr_channel_scan_fwd(const void *x, const void *a, const void *b, c
     gdr_status_t s = scan_sizes(dims, cu_seqlens != nullptr, &z);
     if (s != GDR_OK) return s;
     const gdr_scan_dims_t &d = *dims;
-    const int64_t es = elem_size(d.dtype), need = gdr::scan_fwd_ws_bytes(d.D, z.nseq, z.slots);
+    const int64_t es = elem_size(d.dtype), need = gdr::scan_fwd_ws_bytes(d.T, d.D, z.nseq, cu_seqlens != nullptr);
     s = check_workspace(workspace, workspace_bytes, need);
     if (s != GDR_OK) return s;
     if (cu_seqlens && !aligned(cu_seqlens, 4)) return fail(GDR_ERR_ALIGN, "cu_seqlens is not 4-byte aligned");
@@ -210,7 +210,7 @@ gdr_status_t gdr_channel_scan_bwd(const void *x, const void *a, const void *b, c
     gdr_status_t s = scan_sizes(dims, cu_seqlens != nullptr, &z);
     if (s != GDR_OK) return s;
     const gdr_scan_dims_t &d = *dims;
-    const int64_t es = elem_size(d.dtype), need = gdr::scan_bwd_ws_bytes(d.D, z.nseq, z.slots);
+    const int64_t es = elem_size(d.dtype), need = gdr::scan_bwd_ws_bytes(d.T, d.D, z.nseq, cu_seqlens != nullptr);
     s = check_workspace(workspace, workspace_bytes, need);
     if (s != GDR_OK) return s;
     if (cu_seqlens && !aligned(cu_seqlens, 4)) return fail(GDR_ERR_ALIGN, "cu_seqlens is not 4-byte aligned");

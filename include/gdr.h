@@ -445,7 +445,7 @@ gdr_status_t gdr_gdn2_decode_step(const void *q, const void *k, const void *v,
 typedef struct gdr_scan_dims {
     int64_t B;        /* batch rows; must be 1 when cu_seqlens is given */
     int64_t T;        /* tokens per row (the packed total when cu_seqlens is given) */
-    int64_t D;        /* channels, >= 1 */
+    int64_t D;        /* channels, 1 .. 2^20 */
     int64_t num_seqs; /* segments described by cu_seqlens (ignored when it is NULL) */
     int32_t dtype;    /* gdr_dtype_t of x, a, b, out and their gradients */
     uint32_t flags;   /* GDR_REVERSE: scan each sequence from its last token to its first */

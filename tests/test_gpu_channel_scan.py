@@ -201,3 +201,14 @@ def test_refusals(gdr):
         gdr.channel_scan_fwd(x, a, b, A, dt, out=x)
     with pytest.raises(gdr.GdrError, match="B == 1"):
         gdr.channel_scan_fwd(x, a, b, A, dt, None, torch.zeros(2, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+def test_long_scan_with_the_state_in_place(gdr, reverse):
+    """Few channels, many tokens: the final state written over the initial one must not reach the
+    workgroups that still have to start from it."""
+    x, a, b, A, dt, h, cu = cuda(scan_case([20000, 3000, 0], 32, FP32, 220, packed=True))
+    want, hT, _ = gdr.channel_scan_fwd(x, a, b, A, dt, h, cu, reverse=reverse)
+    state = h.clone()
+    out, same, _ = gdr.channel_scan_fwd(x, a, b, A, dt, state, cu, reverse=reverse, hT=state)
+    assert same is state and torch.equal(out, want) and torch.equal(state, hT)
