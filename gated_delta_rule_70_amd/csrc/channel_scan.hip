@@ -11,7 +11,7 @@
 //
 // A step is the affine map h -> alpha h + beta x, and maps compose: (P, H) over several steps, P the
 // product of their alphas and H the end state from zero. A workgroup owns 16 V neighbouring channels
-// of a sequence (V = 2; 1 where D is odd) and walks it in blocks of 256 tokens: 32 time slots of 8
+// of a sequence and walks it in blocks of 256 tokens: 32 time slots of 8
 // tokens side by side, 16 lanes of V channels each. A thread composes its 8 steps in registers, the
 // slots' maps are joined (shuffles within a wave, LDS between the eight waves, one barrier a
 // block), and the thread runs its steps again from the state that enters them: 8 more
@@ -26,6 +26,7 @@
 // chunks before its own (behind it, in the backward) before it starts, at the cost of reading the
 // inputs of the maps twice.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "gdr_kernels.hpp"
@@ -35,24 +36,38 @@ namespace gdr {
 
 namespace {
 
-// The gates of one element. softplus(u) = max(u, 0) + log1p(z), z = e^{-|u|}; below 2^-5 the
-// logarithm is taken by its series (next term z^5/5 < 2^-27 z), where log(1 + z) would lose z's
-// low bits: the decay's logarithm enters the gradient of A_log by itself.
+// The gates of one element, in base 2: softplus(u) log2 e = max(u, 0) log2 e + log2(1 + z), z =
+// e^{-|u|}. 1 + z is rounded; d is what it lost, and d / (1 + z) (its quotient to a tenth: d is below
+// 2^-24) puts it back, so that small softplus keep their bits: the decay's logarithm enters the
+// gradient of A_log by itself.
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+__device__ __forceinline__ float sigmoid_of(float b) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * b));
+}
+// log2 of alpha; z and 1 + z for the sigmoid of u
+__device__ __forceinline__ float log2_alpha(float u, float rate, float &z, float &w) {
+    z = __builtin_amdgcn_exp2f(-kLog2e * fabsf(u));
+    w = 1.f + z;
+    const float d = z - (w - 1.f);
+    const float l = fmaf(d, fmaf(-0.5f * kLog2e, z, kLog2e), __builtin_amdgcn_logf(w));
+    return -rate * fmaf(__builtin_amdgcn_fmed3f(u, 0.f, INFINITY), kLog2e, l);
+}
+__device__ __forceinline__ float alpha_of(float u, float rate) {
+    float z, w;
+    return __builtin_amdgcn_exp2f(log2_alpha(u, rate, z, w));
+}
 struct Gates {
-    float alpha, beta, la, rs;  // rs = e^{A_log} sigmoid(u)
+    float alpha, beta, la, rs;  // la = log2 alpha, rs = e^{A_log} sigmoid(u)
 };
 __device__ __forceinline__ Gates gates_of(float a, float b, float bias, float rate) {
     const float u = a + bias;
-    const float z = __expf(-fabsf(u));
-    const float series = z * (1.f - z * (0.5f - z * (0.33333333f - z * 0.25f)));
-    const float l1p = z < 0.03125f ? series : __logf(1.f + z);
-    const float inv = __builtin_amdgcn_rcpf(1.f + z);
+    float z, w;
     Gates g;
     // finite, so that la times a vanished alpha is 0
-    g.la = fmaxf(-rate * (fmaxf(u, 0.f) + l1p), -1e30f);
-    g.alpha = __expf(g.la);
-    g.beta = __builtin_amdgcn_rcpf(1.f + __expf(-b));
-    g.rs = rate * (u >= 0.f ? inv : z * inv);
+    g.la = fmaxf(log2_alpha(u, rate, z, w), -1e30f);
+    g.alpha = __builtin_amdgcn_exp2f(g.la);
+    g.beta = sigmoid_of(b);
+    g.rs = rate * (u >= 0.f ? 1.f : z) * __builtin_amdgcn_rcpf(w);
     return g;
 }
 
@@ -117,7 +132,8 @@ struct Lane {
     int wave, sub, col, slot;
     int64_t d0;
     bool on;                 // its channels exist
-    unsigned off[kLen];      // bytes from a block's first row (in memory) to its tokens' channels
+    unsigned off[kLen];      // bytes from a block's first row (in memory) to its tokens' channels (to the
+                             // tile's first where the thread's own do not exist)
     unsigned safe;           // ... to an address that any block with a token has
 
     __device__ __forceinline__ void init(const ScanArgs &a, int64_t tile) {
@@ -133,16 +149,24 @@ struct Lane {
 #pragma unroll
         for (int j = 0; j < kLen; ++j) {
             const int t = slot * kLen + j;
-            off[j] = (rev ? kScanBlock - 1 - t : t) * pitch + (unsigned)(d0 * sizeof(E));
+            off[j] = (rev ? kScanBlock - 1 - t : t) * pitch + (unsigned)((on ? d0 : tile * 16 * V) * sizeof(E));
         }
         safe = rev ? (kScanBlock - 1) * pitch : 0;
     }
     // whether token j of the thread's slot is among the first n of the block
     __device__ __forceinline__ bool has(int j, int n) const { return on && slot * kLen + j < n; }
-    __device__ __forceinline__ void load(Raw (&r)[kLen], const E *p, int n) const {
+    // offsets of the loads of a block of n tokens; tokens it does not have read a safe address
+    __device__ __forceinline__ void places(unsigned (&o)[kLen], int n) const {
 #pragma unroll
-        for (int j = 0; j < kLen; ++j)
-            r[j] = *reinterpret_cast<const Raw *>(reinterpret_cast<const char *>(p) + (has(j, n) ? off[j] : safe));
+        for (int j = 0; j < kLen; ++j) o[j] = off[j];
+        if (n < kScanBlock) {
+#pragma unroll
+            for (int j = 0; j < kLen; ++j) o[j] = has(j, n) ? off[j] : safe;
+        }
+    }
+    __device__ __forceinline__ void load(Raw (&r)[kLen], const E *p, const unsigned (&o)[kLen]) const {
+#pragma unroll
+        for (int j = 0; j < kLen; ++j) r[j] = *reinterpret_cast<const Raw *>(reinterpret_cast<const char *>(p) + o[j]);
     }
     __device__ __forceinline__ void store(E *p, int j, const float (&v)[V]) const {
         Raw r;
@@ -279,9 +303,11 @@ __global__ __launch_bounds__(kThreads, 2) void scan_fwd_kernel(ScanArgs a, ScanP
     auto fetch = [&](int64_t t) __attribute__((always_inline)) {
         const int64_t row = block_row(a, n, t) * a.D;
         const int left = n.t1 - t < kScanBlock ? (int)(n.t1 - t) : kScanBlock;
-        ln.load(rx, (const E *)a.x + row, left);
-        ln.load(ra, (const E *)a.a + row, left);
-        ln.load(rb, (const E *)a.b + row, left);
+        unsigned o[kLen];
+        ln.places(o, left);
+        ln.load(rx, (const E *)a.x + row, o);
+        ln.load(ra, (const E *)a.a + row, o);
+        ln.load(rb, (const E *)a.b + row, o);
     };
     if (n.t0 < n.t1) fetch(n.t0);
     int buf = 0;
@@ -306,17 +332,28 @@ __global__ __launch_bounds__(kThreads, 2) void scan_fwd_kernel(ScanArgs a, ScanP
             H[i] = 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < kLen; ++j) {
-            const bool in = left == kScanBlock || ln.has(j, left);
+        for (int j = 0; j < kLen; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const Gates g = gates_of((float)ga[j][i], (float)gb[j][i], bias[i], rate[i]);
-                al[j][i] = in ? g.alpha : 1.f;
-                v[j][i] = in ? g.beta * (float)x[j][i] : 0.f;
+                al[j][i] = alpha_of((float)ga[j][i] + bias[i], rate[i]);
+                v[j][i] = sigmoid_of((float)gb[j][i]) * (float)x[j][i];
+            }
+        if (left < kScanBlock) {  // past the end: the identity
+#pragma unroll
+            for (int j = 0; j < kLen; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    al[j][i] = ln.has(j, left) ? al[j][i] : 1.f;
+                    v[j][i] = ln.has(j, left) ? v[j][i] : 0.f;
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < kLen; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
                 H[i] = fmaf(al[j][i], H[i], v[j][i]);
                 P[i] *= al[j][i];
             }
-        }
         WaveMap<V> all, before;
         join_in_wave<V, false>(ln.sub, P, H, all, before);
         if (ln.sub == 3) rec[buf][ln.wave][ln.col] = all;
@@ -325,11 +362,19 @@ __global__ __launch_bounds__(kThreads, 2) void scan_fwd_kernel(ScanArgs a, ScanP
         join_waves<V, false>(rec[buf], ln.wave, ln.col, before, carry, whole, h);
         if (MODE == kCompose) continue;
         E *out = (E *)a.out + block_row(a, n, t) * a.D;
+        float hs[kLen][V];
 #pragma unroll
-        for (int j = 0; j < kLen; ++j) {
+        for (int j = 0; j < kLen; ++j)
 #pragma unroll
-            for (int i = 0; i < V; ++i) h[i] = fmaf(al[j][i], h[i], v[j][i]);
-            if (ln.has(j, left)) ln.store(out, j, h);
+            for (int i = 0; i < V; ++i) hs[j][i] = h[i] = fmaf(al[j][i], h[i], v[j][i]);
+        if (left == kScanBlock) {
+            if (ln.on)
+#pragma unroll
+                for (int j = 0; j < kLen; ++j) ln.store(out, j, hs[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kLen; ++j)
+                if (ln.has(j, left)) ln.store(out, j, hs[j]);
         }
     }
     if (ln.slot == 0 && ln.on) {
@@ -378,11 +423,13 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, ScanP
     auto fetch = [&](int64_t t) __attribute__((always_inline)) {
         const int64_t row = block_row(a, n, t) * a.D;
         const int left = n.t1 - t < kScanBlock ? (int)(n.t1 - t) : kScanBlock;
-        ln.load(ra, (const E *)a.a + row, left);
-        ln.load(rg, (const E *)a.dout + row, left);
+        unsigned o[kLen];
+        ln.places(o, left);
+        ln.load(ra, (const E *)a.a + row, o);
+        ln.load(rg, (const E *)a.dout + row, o);
         if (MODE != kCompose) {
-            ln.load(rx, (const E *)a.x + row, left);
-            ln.load(rb, (const E *)a.b + row, left);
+            ln.load(rx, (const E *)a.x + row, o);
+            ln.load(rb, (const E *)a.b + row, o);
         }
     };
     const int64_t blocks = (n.t1 - n.t0 + kScanBlock - 1) / kScanBlock;
@@ -413,21 +460,35 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, ScanP
             H[i] = C[i] = 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < kLen; ++j) {
-            const bool in = left == kScanBlock || ln.has(j, left);
+        for (int j = 0; j < kLen; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                Gates g = gates_of((float)ga[j][i], MODE == kCompose ? 0.f : (float)gb[j][i], bias[i], rate[i]);
-                if (!in) {  // past the end: the identity, with no gradient of its own
-                    g.alpha = 1.f;
-                    g.beta = g.la = g.rs = 0.f;
-                    go[j][i] = (E)0.f;
+                if (MODE == kCompose) q[j][i].alpha = alpha_of((float)ga[j][i] + bias[i], rate[i]);
+                else q[j][i] = gates_of((float)ga[j][i], (float)gb[j][i], bias[i], rate[i]);
+            }
+        if (left < kScanBlock) {  // past the end: the identity, with no gradient of its own
+#pragma unroll
+            for (int j = 0; j < kLen; ++j) {
+                const bool in = ln.has(j, left);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    q[j][i].alpha = in ? q[j][i].alpha : 1.f;
+                    go[j][i] = in ? go[j][i] : (E)0.f;
+                    if (MODE != kCompose) {
+                        q[j][i].beta = in ? q[j][i].beta : 0.f;
+                        q[j][i].la = in ? q[j][i].la : 0.f;
+                        q[j][i].rs = in ? q[j][i].rs : 0.f;
+                    }
                 }
-                q[j][i] = g;
-                if (MODE != kCompose) H[i] = fmaf(g.alpha, H[i], g.beta * (float)x[j][i]);
-                P[i] *= g.alpha;
             }
         }
+#pragma unroll
+        for (int j = 0; j < kLen; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (MODE != kCompose) H[i] = fmaf(q[j][i].alpha, H[i], q[j][i].beta * (float)x[j][i]);
+                P[i] *= q[j][i].alpha;
+            }
 #pragma unroll
         for (int j = kLen - 1; j >= 0; --j)
 #pragma unroll
@@ -471,7 +532,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, ScanP
                 sb[i] += va[i];
                 c[i] = g.alpha * up;
             }
-            if (ln.has(j, left)) {
+            if (left == kScanBlock ? ln.on : ln.has(j, left)) {
                 ln.store(dx, j, vx);
                 ln.store(da, j, va);
                 ln.store(db, j, vb);
@@ -497,7 +558,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, ScanP
             float s = 0.f;
 #pragma unroll
             for (int k = 0; k < kSlots; ++k) s += part[ln.slot][i][k][ln.col];
-            sums[(2 * u + ln.slot) * a.D + ln.d0 + i] = s;
+            sums[(2 * u + ln.slot) * a.D + ln.d0 + i] = ln.slot == 0 ? s * kLn2 : s;  // la was in base 2
         }
     }
     if (ln.slot == 0 && ln.on && a.dh0 && n.c == 0) {
@@ -534,20 +595,23 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= a.nseq * a.D) return;
     const int64_t d = i % a.D;
-    const Gates g = gates_of((float)((const E *)a.a)[i], (float)((const E *)a.b)[i], a.dt_bias[d], expf(a.A_log[d]));
-    const float h = g.alpha * a.h0[i] + g.beta * (float)((const E *)a.x)[i];
+    const float alpha = alpha_of((float)((const E *)a.a)[i] + a.dt_bias[d], expf(a.A_log[d]));
+    const float h = fmaf(alpha, a.h0[i], sigmoid_of((float)((const E *)a.b)[i]) * (float)((const E *)a.x)[i]);
     a.hT[i] = h;
     ((E *)a.out)[i] = (E)h;
 }
 
-int vec_of(int64_t D) { return D % 2 ? 1 : 2; }
+// Channels a thread: 64-byte runs of a row for 16 lanes, as two bf16 a lane or one fp32 (two fp32, a third of
+// whose backward's registers spilled: 0.214 ms against 0.142 ms on packed fp32 sequences of 520 channels);
+// one bf16 where rows are not whole pairs.
+int vec_of(int64_t D, int dtype) { return dtype == kDtypeBf16 && D % 2 == 0 ? 2 : 1; }
 
 // Split where whole sequences would leave compute units idle: fewer than 224 workgroups (of 256), or,
 // packed, fewer than 1024 (their lengths differ and are not known here). Chunks are whole blocks, of a
 // size that gives about 768 workgroups: three a compute unit, which evens out the ends.
-ScanPlan plan_of(int64_t T, int64_t D, int64_t nseq, bool packed) {
+ScanPlan plan_of(int64_t T, int64_t D, int64_t nseq, bool packed, int vec) {
     ScanPlan p;
-    const int64_t cols = 16 * vec_of(D);
+    const int64_t cols = 16 * vec;
     p.ntile = (D + cols - 1) / cols;
     p.chunk = 0;
     p.units = nseq;
@@ -560,11 +624,11 @@ ScanPlan plan_of(int64_t T, int64_t D, int64_t nseq, bool packed) {
     p.units = packed ? T / p.chunk + nseq + 1 : nseq * p.per_seq;
     return p;
 }
-ScanPlan plan_of(const ScanArgs &a) { return plan_of(a.T, a.D, a.nseq, a.cu_seqlens != nullptr); }
+ScanPlan plan_of(const ScanArgs &a, int vec) { return plan_of(a.T, a.D, a.nseq, a.cu_seqlens != nullptr, vec); }
 
 template <typename E, int V>
 hipError_t fwd_t(const ScanArgs &a, hipStream_t s) {
-    const ScanPlan p = plan_of(a);
+    const ScanPlan p = plan_of(a, V);
     const dim3 grid((unsigned)(p.units * p.ntile)), block(kThreads);
     float2 *agg = (float2 *)a.ws;
     if (!p.chunk) {
@@ -580,7 +644,7 @@ hipError_t fwd_t(const ScanArgs &a, hipStream_t s) {
 
 template <typename E, int V>
 hipError_t bwd_t(const ScanArgs &a, hipStream_t s) {
-    const ScanPlan p = plan_of(a);
+    const ScanPlan p = plan_of(a, V);
     const dim3 grid((unsigned)(p.units * p.ntile)), block(kThreads);
     float *sums = a.ws;
     float2 *agg = (float2 *)(a.ws + 2 * p.units * a.D);
@@ -603,24 +667,24 @@ hipError_t bwd_t(const ScanArgs &a, hipStream_t s) {
 
 }  // namespace
 
-int64_t scan_fwd_ws_bytes(int64_t T, int64_t D, int64_t nseq, bool packed) {
-    const ScanPlan p = plan_of(T, D, nseq, packed);
+int64_t scan_fwd_ws_bytes(int64_t T, int64_t D, int64_t nseq, bool packed, int dtype) {
+    const ScanPlan p = plan_of(T, D, nseq, packed, vec_of(D, dtype));
     return p.chunk ? p.units * D * 8 : 0;
 }
-int64_t scan_bwd_ws_bytes(int64_t T, int64_t D, int64_t nseq, bool packed) {
-    const ScanPlan p = plan_of(T, D, nseq, packed);
+int64_t scan_bwd_ws_bytes(int64_t T, int64_t D, int64_t nseq, bool packed, int dtype) {
+    const ScanPlan p = plan_of(T, D, nseq, packed, vec_of(D, dtype));
     return p.units * D * (p.chunk ? 16 : 8);
 }
 
 hipError_t launch_scan_fwd(const ScanArgs &a, int dtype, hipStream_t s) {
     if (a.nseq == 0) return hipSuccess;
-    if (dtype == kDtypeBf16) return vec_of(a.D) == 2 ? fwd_t<__bf16, 2>(a, s) : fwd_t<__bf16, 1>(a, s);
-    return vec_of(a.D) == 2 ? fwd_t<float, 2>(a, s) : fwd_t<float, 1>(a, s);
+    if (dtype == kDtypeBf16) return vec_of(a.D, dtype) == 2 ? fwd_t<__bf16, 2>(a, s) : fwd_t<__bf16, 1>(a, s);
+    return fwd_t<float, 1>(a, s);
 }
 
 hipError_t launch_scan_bwd(const ScanArgs &a, int dtype, hipStream_t s) {
-    if (dtype == kDtypeBf16) return vec_of(a.D) == 2 ? bwd_t<__bf16, 2>(a, s) : bwd_t<__bf16, 1>(a, s);
-    return vec_of(a.D) == 2 ? bwd_t<float, 2>(a, s) : bwd_t<float, 1>(a, s);
+    if (dtype == kDtypeBf16) return vec_of(a.D, dtype) == 2 ? bwd_t<__bf16, 2>(a, s) : bwd_t<__bf16, 1>(a, s);
+    return bwd_t<float, 1>(a, s);
 }
 
 hipError_t launch_scan_step(const ScanArgs &a, int dtype, hipStream_t s) {

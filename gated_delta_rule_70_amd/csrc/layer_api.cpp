@@ -162,13 +162,13 @@ int64_t gdr_channel_scan_states_elems(const gdr_scan_dims_t *dims, int32_t packe
 int64_t gdr_channel_scan_fwd_workspace_bytes(const gdr_scan_dims_t *dims, int32_t packed) {
     ScanSizes z;
     if (scan_sizes(dims, packed != 0, &z) != GDR_OK) return -1;
-    return gdr::scan_fwd_ws_bytes(dims->T, dims->D, z.nseq, packed != 0);
+    return gdr::scan_fwd_ws_bytes(dims->T, dims->D, z.nseq, packed != 0, dims->dtype);
 }
 
 int64_t gdr_channel_scan_bwd_workspace_bytes(const gdr_scan_dims_t *dims, int32_t packed) {
     ScanSizes z;
     if (scan_sizes(dims, packed != 0, &z) != GDR_OK) return -1;
-    return gdr::scan_bwd_ws_bytes(dims->T, dims->D, z.nseq, packed != 0);
+    return gdr::scan_bwd_ws_bytes(dims->T, dims->D, z.nseq, packed != 0, dims->dtype);
 }
 
 gdr_status_t gdr_channel_scan_fwd(const void *x, const void *a, const void *b, const float *A_log, const float *dt_bias,
@@ -179,7 +179,7 @@ gdr_status_t gdr_channel_scan_fwd(const void *x, const void *a, const void *b, c
     gdr_status_t s = scan_sizes(dims, cu_seqlens != nullptr, &z);
     if (s != GDR_OK) return s;
     const gdr_scan_dims_t &d = *dims;
-    const int64_t es = elem_size(d.dtype), need = gdr::scan_fwd_ws_bytes(d.T, d.D, z.nseq, cu_seqlens != nullptr);
+    const int64_t es = elem_size(d.dtype), need = gdr::scan_fwd_ws_bytes(d.T, d.D, z.nseq, cu_seqlens != nullptr, d.dtype);
     s = check_workspace(workspace, workspace_bytes, need);
     if (s != GDR_OK) return s;
     if (cu_seqlens && !aligned(cu_seqlens, 4)) return fail(GDR_ERR_ALIGN, "cu_seqlens is not 4-byte aligned");
@@ -210,7 +210,7 @@ gdr_status_t gdr_channel_scan_bwd(const void *x, const void *a, const void *b, c
     gdr_status_t s = scan_sizes(dims, cu_seqlens != nullptr, &z);
     if (s != GDR_OK) return s;
     const gdr_scan_dims_t &d = *dims;
-    const int64_t es = elem_size(d.dtype), need = gdr::scan_bwd_ws_bytes(d.T, d.D, z.nseq, cu_seqlens != nullptr);
+    const int64_t es = elem_size(d.dtype), need = gdr::scan_bwd_ws_bytes(d.T, d.D, z.nseq, cu_seqlens != nullptr, d.dtype);
     s = check_workspace(workspace, workspace_bytes, need);
     if (s != GDR_OK) return s;
     if (cu_seqlens && !aligned(cu_seqlens, 4)) return fail(GDR_ERR_ALIGN, "cu_seqlens is not 4-byte aligned");

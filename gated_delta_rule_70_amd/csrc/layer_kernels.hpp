@@ -55,8 +55,8 @@ hipError_t launch_scan_fwd(const ScanArgs &a, int dtype, hipStream_t s);
 hipError_t launch_scan_bwd(const ScanArgs &a, int dtype, hipStream_t s);
 // out = one token of nseq sequences: h0 is the state read, hT the state written
 hipError_t launch_scan_step(const ScanArgs &a, int dtype, hipStream_t s);
-int64_t scan_fwd_ws_bytes(int64_t T, int64_t D, int64_t nseq, bool packed);
-int64_t scan_bwd_ws_bytes(int64_t T, int64_t D, int64_t nseq, bool packed);
+int64_t scan_fwd_ws_bytes(int64_t T, int64_t D, int64_t nseq, bool packed, int dtype);
+int64_t scan_bwd_ws_bytes(int64_t T, int64_t D, int64_t nseq, bool packed, int dtype);
 
 hipError_t launch_ffn_fwd(const FfnArgs &a, int dtype, hipStream_t s);
 hipError_t launch_ffn_bwd(const FfnArgs &a, int dtype, hipStream_t s);
