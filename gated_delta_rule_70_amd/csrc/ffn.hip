@@ -88,29 +88,50 @@ hipError_t fwd_t(const FfnArgs &a, hipStream_t s) {
     return launch_gemm<E, true, true, 2>(g, GluEpi<E>{(E *)a.h, (E *)a.gate, (E *)a.up, a.M, a.F, a.act}, s);
 }
 
+// the products of the backward: dx, and both weights' gradients side by side
+template <typename E>
+GemmOp dx_op(const FfnArgs &a, const E *dg, const E *du) {
+    return GemmOp{{dg, du}, {a.wg, a.wu}, grad_ld(a.F), a.D, a.M, a.D, a.F, 2, 1};
+}
+template <typename E>
+GemmOp dw_op(const FfnArgs &a, const E *dg, const E *du) {
+    return GemmOp{{dg, du}, {a.x, a.x}, grad_ld(a.F), a.D, a.F, a.D, a.M, 1, 2};
+}
+// workspace: dG and dU, then the partial products of one product at a time
+template <typename E>
+int64_t bwd_bytes(const FfnArgs &a) {
+    const E *none = nullptr;
+    const int64_t x = store_ws_bytes<E>(dx_op(a, none, none)), w = store_ws_bytes<E>(dw_op(a, none, none));
+    return 2 * a.M * grad_ld(a.F) * (int64_t)sizeof(E) + (x > w ? x : w);
+}
+
 template <typename E>
 hipError_t bwd_t(const FfnArgs &a, hipStream_t s) {
     const int64_t ld = grad_ld(a.F);
     E *dg = (E *)a.ws, *du = dg + a.M * ld;
+    void *part = du + a.M * ld;
     if (a.M > 0) {
         const int64_t blocks = (a.M * ld + 255) / 256;
         hipLaunchKernelGGL((glu_grad_kernel<E>), dim3((unsigned)blocks), dim3(256), 0, s, (const E *)a.gate,
                            (const E *)a.up, (const E *)a.dh, dg, du, a.M, a.F, ld, a.act);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        const GemmOp gx{{dg, du}, {a.wg, a.wu}, ld, a.D, a.M, a.D, a.F, 2};
-        e = launch_gemm<E, true, false, 1>(gx, StoreEpi<E>{{(E *)a.dx, nullptr}, nullptr, nullptr, a.M, a.D, a.D}, s);
+        e = launch_gemm_store<E, true, false>(
+            dx_op(a, dg, du), StoreEpi<E>{{(E *)a.dx, nullptr}, nullptr, nullptr, nullptr, a.M, a.D, a.D}, part, s);
         if (e != hipSuccess) return e;
     }
-    const GemmOp gw{{dg, du}, {a.x, a.x}, ld, a.D, a.F, a.D, a.M, 1, 2};
-    return launch_gemm<E, false, false, 1>(
-        gw, StoreEpi<E>{{(E *)a.dwg, (E *)a.dwu}, nullptr, nullptr, a.F, a.D, a.D}, s);
+    return launch_gemm_store<E, false, false>(
+        dw_op(a, dg, du), StoreEpi<E>{{(E *)a.dwg, (E *)a.dwu}, nullptr, nullptr, nullptr, a.F, a.D, a.D}, part, s);
 }
 
 }  // namespace
 
-int64_t ffn_bwd_ws_bytes(int64_t M, int64_t, int64_t F, int dtype) {
-    return 2 * M * grad_ld(F) * (dtype == kDtypeBf16 ? 2 : 4);
+int64_t ffn_bwd_ws_bytes(int64_t M, int64_t D, int64_t F, int dtype) {
+    FfnArgs a{};
+    a.M = M;
+    a.D = D;
+    a.F = F;
+    return dtype == kDtypeBf16 ? bwd_bytes<__bf16>(a) : bwd_bytes<float>(a);
 }
 
 hipError_t launch_ffn_fwd(const FfnArgs &a, int dtype, hipStream_t s) {

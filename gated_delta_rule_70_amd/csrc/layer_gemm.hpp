@@ -127,12 +127,14 @@ struct TileGemmArgs {
     int64_t lda, ldb;
     int64_t M, N, K;
     int pairs;   // products summed over
-    int batch;   // products side by side (A[0] B[0], A[1] B[1]); the epilogue is told which
+    int batch;   // products side by side (A[0] B[0], A[1] B[1])
+    int slices;  // slices of k, of `kper` blocks each (the last may have fewer): partial products
+    int kper;
     int nm, nn;  // tiles
 };
 constexpr int kComputeUnits = 256;
 // LDS of one wave for 16 rows of results on their way to memory (RowStore)
-constexpr int stage_bytes(int MI) { return MI == 8 ? 16 * (256 + 16) : 16 * (128 + 16); }
+constexpr int stage_bytes(int MI) { return 16 * ((MI == 8 ? 256 : MI == 4 ? 128 : 64) + 16); }
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
@@ -201,16 +203,16 @@ struct Operand {
             }
         }
     }
-    // rows r0 .. of the matrix at p (of `rows` rows)
-    __device__ __forceinline__ void place(const void *p, int64_t ld, int64_t r0, int64_t rows, int64_t K) {
+    // rows r0 .. of the matrix at p (of `rows` rows), from its block `at` on
+    __device__ __forceinline__ void place(const void *p, int64_t ld, int64_t r0, int64_t rows, int64_t K, int at) {
         if constexpr (KC) {
             const int64_t n = rows - r0 < R ? rows - r0 : R;
-            cur = (const char *)uniform((int64_t)p + r0 * ld * es);
-            left = uniform((((n - 1) * ld + K) * es + 15) & ~15);
-            kleft = (int)(K * es);
+            cur = (const char *)uniform((int64_t)p + r0 * ld * es + at * step);
+            left = uniform(((((n - 1) * ld + K) * es + 15) & ~15) - at * step);
+            kleft = (int)(K * es) - at * 128;
         } else {
-            cur = (const char *)uniform((int64_t)p + r0 * es);
-            left = uniform((((K - 1) * ld + rows - r0) * es + 15) & ~15);
+            cur = (const char *)uniform((int64_t)p + r0 * es + at * step);
+            left = uniform(((((K - 1) * ld + rows - r0) * es + 15) & ~15) - at * step);
         }
     }
     // the next block of the operand, then this wave's copy i of it into LDS at `lds` (byte address)
@@ -319,17 +321,18 @@ __global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 
     int tile, tile_end, stride;
     {
         arg_gemm &a = *(arg_gemm *)arg_at(0);
-        const int all = a.nm * a.nn * a.batch, id = blockIdx.x, x = id & 7, q = all >> 3, r = all & 7;
+        const int all = a.nm * a.nn * a.batch * a.slices, id = blockIdx.x, x = id & 7, q = all >> 3, r = all & 7;
         const int first = x * q + (x < r ? x : r);
         tile = first + (id >> 3);
         tile_end = first + q + (x < r ? 1 : 0);
         stride = ((int)gridDim.x - x + 7) >> 3;
     }
-    auto locate = [&](int t, int &tm, int &tn, int &tb) GDR_INLINE {
+    // tz: batch x slices + slice
+    auto locate = [&](int t, int &tm, int &tn, int &tz) GDR_INLINE {
         arg_gemm &a = *(arg_gemm *)arg_at(0);
         const int per = a.nm * a.nn;
-        tb = t / per;
-        t -= tb * per;
+        tz = t / per;
+        t -= tz * per;
         const int span = 8 * a.nn, group = t / span, in = t % span;
         const int high = a.nm - group * 8 < 8 ? a.nm - group * 8 : 8;
         tm = group * 8 + in % high;
@@ -345,28 +348,36 @@ __global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 
     fb.init(wn * TN, lane);
     bool two;  // a sum of two products (never with two B matrices)
     int nkb;   // blocks of one product
+    int slices, kper;
     {
         arg_gemm &a = *(arg_gemm *)arg_at(0);
         A.init(a.lda, wave, lane);
         B.init(a.ldb, bwave, lane);
         two = NB == 1 && a.pairs == 2;
         nkb = (int)((a.K + KB - 1) / KB);
+        slices = a.slices;
+        kper = a.kper;
     }
-    const int total_kb = two ? 2 * nkb : nkb;
+    // blocks of one product in slice z % slices
+    auto blocks_of = [&](int z) GDR_INLINE {
+        const int at = slices == 1 ? 0 : z % slices * kper;
+        return nkb - at < kper ? nkb - at : kper;
+    };
     const unsigned lds0 = __builtin_amdgcn_readfirstlane(
         (unsigned)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char *)&lds[0][0]));
     constexpr int LA = Operand<E, AKC, BM, NW>::L, LB = Operand<E, BKC, BN / NB, NW / NB>::L;
     // The stream of copies: blocks of product copy_pair of tile copy_tile, copy_left of them. Past the
     // last tile the operands have no bytes: the copies read nothing.
-    int copy_tile = tile, copy_pair = 0, copy_left = nkb;
+    int copy_tile = tile, copy_pair = 0, copy_left = 0;
     auto place = [&]() GDR_INLINE {
         const bool some = copy_tile < tile_end;
-        int tm, tn, tb;
-        locate(some ? copy_tile : tile, tm, tn, tb);
+        int tm, tn, tz;
+        locate(some ? copy_tile : tile, tm, tn, tz);
         arg_gemm &a = *(arg_gemm *)arg_at(0);
-        tb |= copy_pair;
-        A.place(tb ? a.A[1] : a.A[0], a.lda, (int64_t)tm * BM, a.M, a.K);
-        B.place(bhalf | tb ? a.B[1] : a.B[0], a.ldb, (int64_t)tn * (BN / NB), a.N, a.K);
+        const int tb = slices == 1 ? tz | copy_pair : tz / slices, at = slices == 1 ? 0 : tz % slices * kper;
+        copy_left = blocks_of(tz);
+        A.place(tb ? a.A[1] : a.A[0], a.lda, (int64_t)tm * BM, a.M, a.K, at);
+        B.place(bhalf | tb ? a.B[1] : a.B[0], a.ldb, (int64_t)tn * (BN / NB), a.N, a.K, at);
         A.left = some ? A.left : 0;
         B.left = some ? B.left : 0;
     };
@@ -374,7 +385,6 @@ __global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 
         A.begin();
         B.begin();
         if (--copy_left == 0) {
-            copy_left = nkb;
             copy_pair = two ? copy_pair ^ 1 : 0;
             if (!copy_pair) copy_tile += stride;
             place();
@@ -461,6 +471,9 @@ __global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 
             each([](floatx4 &p, floatx4 &) GDR_INLINE { asm volatile("" : "+a"(p)); });
             asm volatile("s_nop 7");
         }
+        int tm, tn, tz;
+        locate(tile, tm, tn, tz);
+        const int total_kb = two ? 2 * nkb : blocks_of(tz);
         for (int kb = 0; kb < total_kb; ++kb) {
             multiply(0, [&](int i) GDR_INLINE { read(h, 1, i * NR / MI, (i + 1) * NR / MI); });
             hand_over();
@@ -482,8 +495,6 @@ __global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 
             each([](floatx4 &p, floatx4 &) GDR_INLINE { asm volatile("" : "+a"(p)); });
             asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
         }
-        int tm, tn, tb;
-        locate(tile, tm, tn, tb);
         Epi epi;
         {
             static_assert(sizeof(Epi) % 8 == 0 && alignof(Epi) == 8 && sizeof(TileGemmArgs) % 8 == 0, "argument layout");
@@ -494,7 +505,7 @@ __global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 
             for (int i = 0; i < (int)(sizeof(Epi) / 8); ++i) words[i] = p[i];
             __builtin_memcpy(&epi, words, sizeof(Epi));
         }
-        epi(acc, (int64_t)tm * BM + wm * TM, (int64_t)tn * (BN / NB) + wn * TN, tb, stage[wave]);
+        epi(acc, (int64_t)tm * BM + wm * TM, (int64_t)tn * (BN / NB) + wn * TN, tz, stage[wave]);
     }
     // the copies past the end land before the wave ends
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
@@ -504,9 +515,14 @@ template <typename E, bool AKC, bool BKC, int NB, int BM, int BN, int WM, int WN
 hipError_t launch_gemm_tile(TileGemmArgs a, const Epi &epi, hipStream_t s) {
     const int64_t nm = (a.M + BM - 1) / BM, nn = (a.N + BN / NB - 1) / (BN / NB);
     if (nm * nn == 0) return hipSuccess;
-    const int64_t all = nm * nn * a.batch;
-    if (all > INT32_MAX / 16 || a.K < 1 || a.pairs * a.batch * NB > 2 || a.pairs * a.batch < 1) return hipErrorInvalidValue;
-    constexpr int64_t resident = kComputeUnits * ((BM + BN) * 256 + WM * WN * stage_bytes(BM / WM / 16) > 81920 ? 1 : 2);
+    const int64_t all = nm * nn * a.batch * a.slices, nkb = (a.K * (int64_t)sizeof(E) + 127) / 128;
+    if (all > INT32_MAX / 16 || a.K < 1 || a.pairs * a.batch * NB > 2 || a.pairs * a.batch < 1 || nkb > INT32_MAX / 4 ||
+        a.slices < 1 || (a.pairs > 1 && a.slices > 1))
+        return hipErrorInvalidValue;
+    // slices of whole blocks, none of them empty
+    a.kper = (int)((nkb + a.slices - 1) / a.slices);
+    if ((int64_t)a.kper * (a.slices - 1) >= nkb) return hipErrorInvalidValue;
+    constexpr int64_t resident = kComputeUnits * (163840 / ((BM + BN) * 256 + WM * WN * stage_bytes(BM / WM / 16)));
     a.nm = (int)nm;
     a.nn = (int)nn;
     hipLaunchKernelGGL((gemm_tile_kernel<E, AKC, BKC, NB, BM, BN, WM, WN, Epi>), dim3((unsigned)(all < resident ? all : resident)),
@@ -514,7 +530,7 @@ hipError_t launch_gemm_tile(TileGemmArgs a, const Epi &epi, hipStream_t s) {
     return hipGetLastError();
 }
 
-// columns of C per wave are a multiple of this in the tiled and in the any-size kernel
+// columns of C per partial sum of a wave (linear_ce.hip) in the tiled and in the any-size kernel
 constexpr int kTileCols = 64, kAnyCols = 32;
 
 // C = sum of A_p B_p^T in the order given by AKC and BKC (true: k contiguous, the leading dimension
@@ -523,20 +539,30 @@ struct GemmOp {
     const void *A[2], *B[2];
     int64_t lda, ldb, M, N, K;
     int pairs = 1, batch = 1;  // at most one of them 2: A[0] B[0] + A[1] B[1], or the two side by side
+    int slices = 1;            // of k: the epilogue gets partial products (batch x slices + slice)
 };
 // whether rows of ld elements are whole 16-byte pieces
 template <typename E>
 bool whole_pieces(int64_t ld) {
     return ld * (int64_t)sizeof(E) % 16 == 0;
 }
+// The tile: 256 x 256 (one workgroup a compute unit) from 192 tiles on; below, 128 x 128 (two) while there
+// are 384 of them; below, 64 x 128 (three). Fewer, larger tiles read less and multiply faster, but
+// leave compute units idle: (feed-forward forward, 2048 x 8192) 256 tokens took 27.2 us in 256 tiles of
+// 128 x 128. fp32 products are bound by the matrix instructions at 128 x 128 already.
+inline int tile_of(int64_t M, int64_t N, int parts, bool bf16) {
+    if (bf16 && ((M + 255) / 256) * ((N + 255) / 256) * parts >= 192) return 256;
+    return ((M + 127) / 128) * ((N + 127) / 128) * parts >= 384 ? 128 : 64;
+}
 template <typename E, bool AKC, bool BKC, int NB, class Epi>
 hipError_t launch_gemm(const GemmOp &o, const Epi &epi, hipStream_t s) {
     if (whole_pieces<E>(o.lda) && whole_pieces<E>(o.ldb) && o.K > 0) {
-        const TileGemmArgs t{{o.A[0], o.A[1]}, {o.B[0], o.B[1]}, o.lda, o.ldb, o.M, o.N, o.K, o.pairs, o.batch, 0, 0};
-        const int64_t big = ((o.M + 255) / 256) * ((o.N * NB + 255) / 256) * o.batch;
+        const TileGemmArgs t{{o.A[0], o.A[1]}, {o.B[0], o.B[1]}, o.lda, o.ldb, o.M, o.N, o.K, o.pairs, o.batch, o.slices, 0, 0, 0};
+        const int tile = tile_of(o.M, o.N * NB, o.batch * o.slices, sizeof(E) == 2);
         if constexpr (sizeof(E) == 2)
-            if (big >= 192) return launch_gemm_tile<E, AKC, BKC, NB, 256, 256, 2, 2>(t, epi, s);
-        return launch_gemm_tile<E, AKC, BKC, NB, 128, 128, 2, 2>(t, epi, s);
+            if (tile == 256) return launch_gemm_tile<E, AKC, BKC, NB, 256, 256, 2, 2>(t, epi, s);
+        if (tile == 128) return launch_gemm_tile<E, AKC, BKC, NB, 128, 128, 2, 2>(t, epi, s);
+        return launch_gemm_tile<E, AKC, BKC, NB, 64, 128, 2, 2>(t, epi, s);
     }
     for (int b = 0; b < o.batch; ++b) {
         const AnyGemmArgs g{{o.A[b], o.A[1]}, {o.B[b], o.B[1]}, AKC ? o.lda : 1, AKC ? 1 : o.lda, BKC ? o.ldb : 1,
@@ -613,17 +639,20 @@ __device__ __forceinline__ void store_rows(char *st, const floatx4 (&v)[NI], E *
     }
 }
 
-// C = (acc_in +) the product, rounded to E in out[batch], or kept in 32 bits in `acc_out`.
+// C = (acc_in +) the product, rounded to E in out[batch], or kept in 32 bits in `acc_out`; a slice of k goes
+// to `part` [batch x slices][M][ld] as it is.
 template <typename E>
 struct StoreEpi {
     E *out[2];
     const float *acc_in;
     float *acc_out;
+    float *part;
     int64_t M, N, ld;
     template <int MI, int NI>
-    __device__ __forceinline__ void operator()(const floatx4 (&acc)[1][MI][NI], int64_t m0, int64_t n0, int batch, char *st) const {
+    __device__ __forceinline__ void operator()(const floatx4 (&acc)[1][MI][NI], int64_t m0, int64_t n0, int z, char *st) const {
         const int lane = epilogue_lane(), g = lane >> 4, c = lane & 15;
-        E *C = batch ? out[1] : out[0];
+        E *C = part ? nullptr : z ? out[1] : out[0];
+        float *C32 = part ? part + z * M * ld : acc_out;
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             floatx4 v[NI];
@@ -642,9 +671,68 @@ struct StoreEpi {
                 }
             }
             if (C) store_rows<E, MI, NI>(st, v, C, ld, m0 + 16 * i, n0, M, N);
-            else store_rows<float, MI, NI>(st, v, acc_out, ld, m0 + 16 * i, n0, M, N);
+            else store_rows<float, MI, NI>(st, v, C32, ld, m0 + 16 * i, n0, M, N);
         }
     }
 };
+
+// C[b] = (acc_in +) the sum of its `parts` partial products, in order; four neighbours a thread. n: elements
+// of one product, a multiple of 4.
+template <typename E>
+__global__ __launch_bounds__(256) void gemm_sum_kernel(const float *part, int parts, int64_t n, E *out0, E *out1,
+                                                       const float *acc_in, float *acc_out) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    const int b = blockIdx.y;
+    floatx4 v = acc_in ? *reinterpret_cast<const floatx4 *>(acc_in + i) : zero4();
+    for (int p = 0; p < parts; ++p) v += *reinterpret_cast<const floatx4 *>(part + ((int64_t)b * parts + p) * n + i);
+    E *out = b ? out1 : out0;
+    if (out) *reinterpret_cast<typename Vec4<E>::type *>(out + i) = cvt4<E>(v);
+    else *reinterpret_cast<floatx4 *>(acc_out + i) = v;
+}
+
+// Slices of k of a plain product (rows of N elements): where the tiles of 128 x 128 (256 x 256 in bf16) do not
+// fill the compute units, k is cut so that they do, into slices of at least eight blocks. Each
+// slice costs a write and a read of C in 32 bits. A sum of two products is cut at the seam first.
+// (Cross entropy, 1021 tokens x 1024, vocabulary 32003: dx is 64 tiles of 501 blocks, 388 us uncut.)
+template <typename E>
+int slices_of(int64_t lda, int64_t ldb, int64_t M, int64_t N, int64_t K, int products) {
+    if (!whole_pieces<E>(lda) || !whole_pieces<E>(ldb) || N % 4 || M < 1 || K < 1) return 1;
+    if (tile_of(M, N, products, sizeof(E) == 2) == 256) return 1;
+    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128) * products, nkb = (K * (int64_t)sizeof(E) + 127) / 128;
+    int64_t s = 512 / tiles;
+    if (s > nkb / 8) s = nkb / 8;
+    if (s > 32) s = 32;
+    if (s < 2) return 1;
+    const int64_t kper = (nkb + s - 1) / s;
+    return (int)((nkb + kper - 1) / kper);  // none of them empty
+}
+// bytes of partial products launch_gemm_store needs
+template <typename E>
+int64_t store_ws_bytes(const GemmOp &o) {
+    const int products = o.pairs * o.batch, s = slices_of<E>(o.lda, o.ldb, o.M, o.N, o.K, products);
+    return s > 1 ? s * products * o.M * o.N * 4 : 0;
+}
+// The plain product (epi.part is set here), cut where slices_of says so.
+template <typename E, bool AKC, bool BKC>
+hipError_t launch_gemm_store(const GemmOp &o, StoreEpi<E> epi, void *ws, hipStream_t s) {
+    epi.part = nullptr;
+    const int products = o.pairs * o.batch, slices = slices_of<E>(o.lda, o.ldb, o.M, o.N, o.K, products);
+    if (slices == 1) return launch_gemm<E, AKC, BKC, 1>(o, epi, s);
+    if (epi.ld != o.N) return hipErrorInvalidValue;
+    GemmOp cut = o;
+    cut.pairs = 1;
+    cut.batch = products;
+    cut.slices = slices;
+    StoreEpi<E> to_part = epi;
+    to_part.part = (float *)ws;
+    to_part.acc_in = nullptr;
+    const hipError_t e = launch_gemm<E, AKC, BKC, 1>(cut, to_part, s);
+    if (e != hipSuccess) return e;
+    const int64_t n = o.M * o.N;
+    hipLaunchKernelGGL((gemm_sum_kernel<E>), dim3((unsigned)((n / 4 + 255) / 256), (unsigned)o.batch), dim3(256), 0, s, (const float *)ws,
+                       slices * o.pairs, n, epi.out[0], epi.out[1], epi.acc_in, epi.acc_out);
+    return hipGetLastError();
+}
 
 }  // namespace gdr

@@ -13,6 +13,7 @@
 // dW's rows of the piece are complete and dx is summed over the pieces in 32 bits.
 #include <hip/hip_runtime.h>
 #include <math.h>
+#include <initializer_list>
 #include <type_traits>
 #include <stdint.h>
 
@@ -209,11 +210,44 @@ hipError_t fwd_t(const CeArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// the products of one piece of the backward (`width` columns from w)
+template <typename E>
+GemmOp dw_op(const CeArgs &a, const E *dl, int64_t piece, int64_t width) {
+    return GemmOp{{dl, nullptr}, {a.x, nullptr}, piece, a.D, width, a.D, a.N};
+}
+template <typename E>
+GemmOp dx_op(const CeArgs &a, const E *dl, const E *w, int64_t piece, int64_t width) {
+    return GemmOp{{dl, nullptr}, {w, nullptr}, piece, a.D, a.N, a.D, width};
+}
+// workspace: dl of a piece, dx in 32 bits where there are several, the partial products of one product
+// at a time
+struct BwdLayout {
+    int64_t acc, part, total;
+};
+template <typename E>
+BwdLayout bwd_layout(const CeArgs &a) {
+    const int64_t piece = piece_of(a.N, a.V), tail = a.V % piece ? a.V % piece : piece;
+    const E *none = nullptr;
+    int64_t part = 0;
+    for (int64_t width : {piece < a.V ? piece : a.V, tail}) {
+        const int64_t w = store_ws_bytes<E>(dw_op(a, none, piece, width)), x = store_ws_bytes<E>(dx_op(a, none, none, piece, width));
+        part = part > w ? part : w;
+        part = part > x ? part : x;
+    }
+    BwdLayout l;
+    l.acc = up256(a.N * piece * (int64_t)sizeof(E));
+    l.part = l.acc + (piece < a.V ? up256(a.N * a.D * 4) : 0);
+    l.total = l.part + part;
+    return l;
+}
+
 template <typename E>
 hipError_t bwd_t(const CeArgs &a, hipStream_t s) {
     const int64_t piece = piece_of(a.N, a.V);
+    const BwdLayout l = bwd_layout<E>(a);
     E *dl = (E *)a.ws;
-    float *acc = (float *)((char *)a.ws + up256(a.N * piece * (int64_t)sizeof(E)));
+    float *acc = (float *)((char *)a.ws + l.acc);
+    void *part = (char *)a.ws + l.part;
     for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
         const int64_t width = a.V - v0 < piece ? a.V - v0 : piece;
         const E *w = (const E *)a.w + v0 * a.D;
@@ -221,13 +255,14 @@ hipError_t bwd_t(const CeArgs &a, hipStream_t s) {
         hipError_t e = launch_gemm<E, true, true, 1>(
             gl, GradEpi<E>{a.t, a.lse_in, a.dloss, dl, a.N, a.V, v0, width, piece}, s);
         if (e != hipSuccess) return e;
-        const GemmOp gw{{dl, nullptr}, {a.x, nullptr}, piece, a.D, width, a.D, a.N};
-        e = launch_gemm<E, false, false, 1>(gw, StoreEpi<E>{{(E *)a.dw + v0 * a.D, nullptr}, nullptr, nullptr, width, a.D, a.D}, s);
+        e = launch_gemm_store<E, false, false>(
+            dw_op(a, dl, piece, width),
+            StoreEpi<E>{{(E *)a.dw + v0 * a.D, nullptr}, nullptr, nullptr, nullptr, width, a.D, a.D}, part, s);
         if (e != hipSuccess) return e;
         const bool last = v0 + piece >= a.V;
-        const GemmOp gx{{dl, nullptr}, {w, nullptr}, piece, a.D, a.N, a.D, width};
-        e = launch_gemm<E, true, false, 1>(
-            gx, StoreEpi<E>{{last ? (E *)a.dx : nullptr, nullptr}, v0 ? acc : nullptr, acc, a.N, a.D, a.D}, s);
+        e = launch_gemm_store<E, true, false>(
+            dx_op(a, dl, w, piece, width),
+            StoreEpi<E>{{last ? (E *)a.dx : nullptr, nullptr}, v0 ? acc : nullptr, acc, nullptr, a.N, a.D, a.D}, part, s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -240,8 +275,11 @@ int64_t ce_fwd_ws_bytes(int64_t N, int64_t D, int64_t V, int dtype) {
     return up256(N * 4) + strips * N * 8;
 }
 int64_t ce_bwd_ws_bytes(int64_t N, int64_t D, int64_t V, int dtype) {
-    const int64_t piece = piece_of(N, V);
-    return up256(N * piece * (dtype == kDtypeBf16 ? 2 : 4)) + (piece < V ? N * D * 4 : 0);
+    CeArgs a{};
+    a.N = N;
+    a.D = D;
+    a.V = V;
+    return dtype == kDtypeBf16 ? bwd_layout<__bf16>(a).total : bwd_layout<float>(a).total;
 }
 
 hipError_t launch_ce_fwd(const CeArgs &a, int dtype, hipStream_t s) {
