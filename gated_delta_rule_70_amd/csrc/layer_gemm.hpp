@@ -98,9 +98,9 @@ hipError_t launch_gemm_any(const AnyGemmArgs &a, const Epi &epi, hipStream_t s) 
 // The tiled product for operands whose rows are multiples of 16 bytes (every pointer of the C ABI
 // is 16-byte aligned, so whole 16-byte pieces are inside or outside a matrix).
 //
-// A workgroup of WM x WN waves computes BM x (BN / NB) columns of C; a block of 128 bytes of k (64 bf16
-// or 32 fp32) of both operands is copied straight from global memory into one half of LDS while
-// the other half is multiplied, one barrier a block. An operand
+// A workgroup of WM x WN waves computes BM x (BN / NB) columns of C; blocks of 128 bytes of k (64 bf16 or
+// 32 fp32) of both operands are copied straight from global memory into a ring of S slots of LDS, one
+// barrier a block. An operand
 // comes in either order:
 //   KC (k contiguous, rows of ld elements): LDS holds rows of 128 bytes, eight 16-byte pieces, piece p
 //      of row r at p ^ (r & 7), so that the 16 rows a fragment read touches spread over the banks;
@@ -297,11 +297,11 @@ __device__ __forceinline__ void mma_step_agpr(floatx4 &acc, bf16x8 a, bf16x8 b) 
     asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
 
-template <typename E, bool AKC, bool BKC, int NB, int BM, int BN, int WM, int WN, class Epi>
+template <typename E, bool AKC, bool BKC, int NB, int BM, int BN, int WM, int WN, int S, class Epi>
 __global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 : 2) void gemm_tile_kernel(TileGemmArgs, Epi) {
     constexpr int NW = WM * WN, TM = BM / WM, TN = BN / NB / WN, MI = TM / 16, NI = TN / 16, KB = 128 / (int)sizeof(E);
     static_assert(NB == 1 || BKC, "two B matrices come k contiguous");
-    __shared__ __align__(1024) char lds[2][(BM + BN) * 128];
+    __shared__ __align__(1024) char lds[S][(BM + BN) * 128];
     __shared__ __align__(16) char stage[NW][stage_bytes(MI)];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -390,7 +390,7 @@ __global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 
             place();
         }
     };
-    // this wave's copies i0 .. i1 - 1 of the LA + LB of the block begun, into half `h` of LDS
+    // this wave's copies i0 .. i1 - 1 of the LA + LB of the block begun, into slot h of the ring
     auto copy = [&](int h, int i0, int i1) GDR_INLINE {
         const unsigned at = lds0 + h * (BM + BN) * 128;
 #pragma unroll
@@ -418,7 +418,7 @@ __global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 
 
     // fragments of the two halves of a block
     typename Fragments<E, AKC, BM, MI>::type va[2][MI], vb[2][NB * NI];
-    // reads i0 .. i1 - 1 of the NB NI + MI of half ks of the block in half h of LDS
+    // reads i0 .. i1 - 1 of the NB NI + MI of half ks of the block in slot h
     auto read = [&](int h, int ks, int i0, int i1) GDR_INLINE {
         const char *buf = lds[h];
 #pragma unroll
@@ -444,23 +444,27 @@ __global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    // this wave's copies have landed and its reads of the block in use are done, then everyone's
-    auto hand_over = []() GDR_INLINE {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    // The first half of a block is multiplied while its second half is read from LDS; then its slot changes
+    // hands, and the second half is multiplied while the next block's first is read and the block S
+    // later is copied into the slot. At the hand-over this wave's reads of the block are done and its
+    // copies of the next block have landed (those of the S - 2 blocks after it may be in flight, and
+    // whatever an epilogue issued since only makes the wait longer), then everyone's.
+    constexpr int NR = NB * NI + MI, NC = LA + LB;
+    auto hand_over = [&]() GDR_INLINE {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"((S - 2) * NC) : "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
-    // The first half of a block is multiplied while its second half is read from LDS; then the halves
-    // of LDS change hands, and the second half is multiplied while the next block's first is read
-    // and the block after it is copied in.
-    constexpr int NR = NB * NI + MI, NC = LA + LB;
-    int h = 0;  // the half of LDS in use
+    int h = 0;  // the slot in use
     place();
-    begin_copy();
-    copy(0, 0, NC);
-    hand_over();
-    begin_copy();
-    copy(1, 0, NC);
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+        begin_copy();
+        copy(i, 0, NC);
+    }
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"((S - 1) * NC) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
     read(0, 0, 0, NR);
     for (; tile < tile_end; tile += stride) {
         each([](floatx4 &p, floatx4 &t) GDR_INLINE {
@@ -478,11 +482,12 @@ __global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 
             multiply(0, [&](int i) GDR_INLINE { read(h, 1, i * NR / MI, (i + 1) * NR / MI); });
             hand_over();
             begin_copy();
+            const int next = h + 1 == S ? 0 : h + 1;
             multiply(1, [&](int i) GDR_INLINE {
-                read(h ^ 1, 0, i * NR / MI, (i + 1) * NR / MI);
+                read(next, 0, i * NR / MI, (i + 1) * NR / MI);
                 copy(h, i * NC / MI, (i + 1) * NC / MI);
             });
-            h ^= 1;
+            h = next;
             if constexpr (blocked)
                 if ((kb + 1) % (kSumK / KB) == 0) each([](floatx4 &p, floatx4 &t) GDR_INLINE {
                     t += p;
@@ -511,7 +516,7 @@ __global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 }
 
-template <typename E, bool AKC, bool BKC, int NB, int BM, int BN, int WM, int WN, class Epi>
+template <typename E, bool AKC, bool BKC, int NB, int BM, int BN, int WM, int WN, int S, class Epi>
 hipError_t launch_gemm_tile(TileGemmArgs a, const Epi &epi, hipStream_t s) {
     const int64_t nm = (a.M + BM - 1) / BM, nn = (a.N + BN / NB - 1) / (BN / NB);
     if (nm * nn == 0) return hipSuccess;
@@ -522,10 +527,10 @@ hipError_t launch_gemm_tile(TileGemmArgs a, const Epi &epi, hipStream_t s) {
     // slices of whole blocks, none of them empty
     a.kper = (int)((nkb + a.slices - 1) / a.slices);
     if ((int64_t)a.kper * (a.slices - 1) >= nkb) return hipErrorInvalidValue;
-    constexpr int64_t resident = kComputeUnits * (163840 / ((BM + BN) * 256 + WM * WN * stage_bytes(BM / WM / 16)));
+    constexpr int64_t resident = kComputeUnits * (163840 / (S * (BM + BN) * 128 + WM * WN * stage_bytes(BM / WM / 16)));
     a.nm = (int)nm;
     a.nn = (int)nn;
-    hipLaunchKernelGGL((gemm_tile_kernel<E, AKC, BKC, NB, BM, BN, WM, WN, Epi>), dim3((unsigned)(all < resident ? all : resident)),
+    hipLaunchKernelGGL((gemm_tile_kernel<E, AKC, BKC, NB, BM, BN, WM, WN, S, Epi>), dim3((unsigned)(all < resident ? all : resident)),
                        dim3(64 * WM * WN), 0, s, a, epi);
     return hipGetLastError();
 }
@@ -648,9 +653,9 @@ hipError_t launch_gemm(const GemmOp &o, const Epi &epi, hipStream_t s) {
         }
         const int tile = tile_of(o.M, o.N * NB, o.batch * o.slices, sizeof(E) == 2);
         if constexpr (sizeof(E) == 2)
-            if (tile == 256) return launch_gemm_tile<E, AKC, BKC, NB, 256, 256, 2, 2>(t, epi, s);
-        if (tile == 128) return launch_gemm_tile<E, AKC, BKC, NB, 128, 128, 2, 2>(t, epi, s);
-        return launch_gemm_tile<E, AKC, BKC, NB, 64, 128, 2, 2>(t, epi, s);
+            if (tile == 256) return launch_gemm_tile<E, AKC, BKC, NB, 256, 256, 2, 2, 2>(t, epi, s);
+        if (tile == 128) return launch_gemm_tile<E, AKC, BKC, NB, 128, 128, 2, 2, 2>(t, epi, s);
+        return launch_gemm_tile<E, AKC, BKC, NB, 64, 128, 2, 2, 3>(t, epi, s);
     }
     for (int b = 0; b < o.batch; ++b) {
         const AnyGemmArgs g{{o.A[b], o.A[1]}, {o.B[b], o.B[1]}, AKC ? o.lda : 1, AKC ? 1 : o.lda, BKC ? o.ldb : 1,
