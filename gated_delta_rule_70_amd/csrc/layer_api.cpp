@@ -79,8 +79,8 @@ gdr_status_t scan_sizes(const gdr_scan_dims_t *dims, bool packed, ScanSizes *z) 
     const gdr_status_t s = check_dtype(d.dtype);
     if (s != GDR_OK) return s;
     if (d.flags & ~GDR_REVERSE) return fail(GDR_ERR_FLAGS, "flags 0x%x: the channel scan takes GDR_REVERSE only", d.flags);
-    if (d.B < 0 || d.T < 0 || d.D < 1 || d.D > kMaxWidth)
-        return fail(GDR_ERR_DIMS, "B (%lld) and T (%lld) must be >= 0 and D (%lld) in [1, 2^20]", (long long)d.B, (long long)d.T, (long long)d.D);
+    if (d.B < 0 || d.T < 0 || d.D < 1)
+        return fail(GDR_ERR_DIMS, "B (%lld) and T (%lld) must be >= 0 and D (%lld) >= 1", (long long)d.B, (long long)d.T, (long long)d.D);
     if (d.T > INT32_MAX) return fail(GDR_ERR_DIMS, "T must be below 2^31");
     z->nseq = d.B;
     if (packed) {
@@ -95,6 +95,7 @@ gdr_status_t scan_sizes(const gdr_scan_dims_t *dims, bool packed, ScanSizes *z) 
     if (z->n < 0 || z->ns < 0 || z->slots < 0 || z->n > (INT64_C(1) << 58) || z->ns > (INT64_C(1) << 58) ||
         prod({z->slots, d.D}) < 0 || prod({z->slots, d.D}) > (INT64_C(1) << 58))
         return fail(GDR_ERR_DIMS, "sizes overflow");
+    if (d.D > kMaxWidth) return fail(GDR_ERR_DIMS, "D (%lld) must be at most 2^20", (long long)d.D);
     // the launches hold a block per (sequence or block of tokens, 16 channels) at most
     if (prod({z->nseq + z->slots, (d.D + 15) / 16}) > INT32_MAX)
         return fail(GDR_ERR_DIMS, "too many sequences or channels");
