@@ -134,11 +134,11 @@ hipError_t bwd_t(const FfnArgs &a, hipStream_t s) {
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         e = launch_gemm_store<E, true, false>(
-            dx_op(a, dg, du), StoreEpi<E>{{(E *)a.dx, nullptr}, nullptr, nullptr, nullptr, a.M, a.D, a.D}, part, s);
+            dx_op(a, dg, du), StoreEpi<E>{{(E *)a.dx, nullptr}, nullptr, nullptr, nullptr, nullptr, a.M, a.D, a.D}, part, s);
         if (e != hipSuccess) return e;
     }
     return launch_gemm_store<E, false, false>(
-        dw_op(a, dg, du), StoreEpi<E>{{(E *)a.dwg, (E *)a.dwu}, nullptr, nullptr, nullptr, a.F, a.D, a.D}, part, s);
+        dw_op(a, dg, du), StoreEpi<E>{{(E *)a.dwg, (E *)a.dwu}, nullptr, nullptr, nullptr, nullptr, a.F, a.D, a.D}, part, s);
 }
 
 }  // namespace

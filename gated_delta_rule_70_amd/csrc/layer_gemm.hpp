@@ -733,20 +733,22 @@ __device__ __forceinline__ void store_rows(char *st, const floatx4 (&v)[NI], E *
     }
 }
 
-// C = (acc_in +) the product, rounded to E in out[batch], or kept in 32 bits in `acc_out`; a slice of k goes
-// to `part` [batch x slices][M][ld] as it is.
+// C = (acc_in +) the product, times *scale (where given) and rounded to E in out[batch], or kept in 32 bits
+// in `acc_out`; a slice of k goes to `part` [batch x slices][M][ld] as it is.
 template <typename E>
 struct StoreEpi {
     E *out[2];
     const float *acc_in;
     float *acc_out;
     float *part;
+    const float *scale;
     int64_t M, N, ld;
     template <int MI, int NI>
     __device__ __forceinline__ void operator()(const floatx4 (&acc)[1][MI][NI], int64_t m0, int64_t n0, int z, char *st) const {
         const int lane = epilogue_lane(), g = lane >> 4, c = lane & 15;
         E *C = part ? nullptr : z ? out[1] : out[0];
         float *C32 = part ? part + z * M * ld : acc_out;
+        const float by = C && scale ? *scale : 1.f;
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             floatx4 v[NI];
@@ -763,6 +765,7 @@ struct StoreEpi {
                         for (int r = 0; r < 4; ++r)
                             if (n + r < N) v[j][r] += p[r];
                 }
+                v[j] *= by;
             }
             if (C) store_rows<E, MI, NI>(st, v, C, ld, m0 + 16 * i, n0, M, N);
             else store_rows<float, MI, NI>(st, v, C32, ld, m0 + 16 * i, n0, M, N);
@@ -774,14 +777,14 @@ struct StoreEpi {
 // of one product, a multiple of 4.
 template <typename E>
 __global__ __launch_bounds__(256) void gemm_sum_kernel(const float *part, int parts, int64_t n, E *out0, E *out1,
-                                                       const float *acc_in, float *acc_out) {
+                                                       const float *acc_in, float *acc_out, const float *scale) {
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= n) return;
     const int b = blockIdx.y;
     floatx4 v = acc_in ? *reinterpret_cast<const floatx4 *>(acc_in + i) : zero4();
     for (int p = 0; p < parts; ++p) v += *reinterpret_cast<const floatx4 *>(part + ((int64_t)b * parts + p) * n + i);
     E *out = b ? out1 : out0;
-    if (out) *reinterpret_cast<typename Vec4<E>::type *>(out + i) = cvt4<E>(v);
+    if (out) *reinterpret_cast<typename Vec4<E>::type *>(out + i) = cvt4<E>(scale ? v * *scale : v);
     else *reinterpret_cast<floatx4 *>(acc_out + i) = v;
 }
 
@@ -825,7 +828,7 @@ hipError_t launch_gemm_store(const GemmOp &o, StoreEpi<E> epi, void *ws, hipStre
     if (e != hipSuccess) return e;
     const int64_t n = o.M * o.N;
     hipLaunchKernelGGL((gemm_sum_kernel<E>), dim3((unsigned)((n / 4 + 255) / 256), (unsigned)o.batch), dim3(256), 0, s, (const float *)ws,
-                       slices * o.pairs, n, epi.out[0], epi.out[1], epi.acc_in, epi.acc_out);
+                       slices * o.pairs, n, epi.out[0], epi.out[1], epi.acc_in, epi.acc_out, epi.scale);
     return hipGetLastError();
 }
 

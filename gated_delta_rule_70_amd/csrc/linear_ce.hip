@@ -9,7 +9,7 @@
 // Forward: each wave reduces its tile of logits to one (max, sum of e^{l - max}) per token, in 32
 // bits, and the lane that holds the target's logit writes it out; a second kernel joins the
 // partial sums of a token. Backward: for each piece of the vocabulary the logits are formed again
-// and turned into dl (in the inputs' type, as the operand of two products), then
+// and turned into dl (in the inputs' type, as the operand of two products, its common factor apart), then
 // dW's rows of the piece are complete and dx is summed over the pieces in 32 bits.
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -108,12 +108,14 @@ template <typename E>
 struct GradEpi {
     const int64_t *t;
     const float *lse, *dloss;
+    const float *inv;  // 1 / the factor taken out of dl
     E *dl;
     int64_t M, V, v0, width, ld;
     template <int MI, int NI>
     __device__ __forceinline__ void operator()(const floatx4 (&acc)[1][MI][NI], int64_t m0, int64_t n0, int, char *st) const {
         const int lane = epilogue_lane(), g = lane >> 4, c = lane & 15;
         float ls[MI], sc[MI];
+        const float inv_scale = *inv;
         int want[MI], left[MI];  // the target's column and the piece's end, from this wave's first column
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
@@ -121,7 +123,7 @@ struct GradEpi {
             const int64_t tm = m < M ? t[m] : -1, tv = tm - v0 - n0;
             const bool on = tm >= 0 && tm < V;
             ls[i] = on ? lse[m] : 0.f;
-            sc[i] = on ? dloss[m] : 0.f;
+            sc[i] = on ? dloss[m] * inv_scale : 0.f;
             want[i] = tv >= 0 && tv < 16 * NI ? (int)tv : -1;
             left[i] = !on ? 0 : width - n0 < 16 * NI ? (int)(width - n0) : 16 * NI;
         }
@@ -153,6 +155,29 @@ struct GradEpi {
         }
     }
 };
+
+// The largest |dloss| of a token that bears a loss, and its inverse (1 and 1 where there is none). It is taken out of dl before
+// dl is rounded to the inputs' type and multiplied back into dx and dW, in 32 bits: with a mean over tokens
+// every dloss is the same number, whose rounding would be a common error of all of dl (2.9e-3 of dW in bf16
+// against 64 bits; without it the large entries, p - 1 at the targets, are near -1 and lose little).
+__global__ __launch_bounds__(1024) void ce_scale_kernel(const float *dloss, const int64_t *t, int64_t N, int64_t V, float *scale) {
+    __shared__ float held[16];
+    float top = 0.f;
+#pragma unroll 4
+    for (int64_t n = threadIdx.x; n < N; n += 1024)
+        if (t[n] >= 0 && t[n] < V) top = fmaxf(top, fabsf(dloss[n]));
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+    if ((threadIdx.x & 63) == 0) held[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x) return;
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, held[i]);
+    // a factor whose inverse is a normal number
+    const bool fit = top > 1e-37f && top < 1e37f;
+    scale[0] = fit ? top : 1.f;
+    scale[1] = fit ? 1.f / top : 1.f;
+}
 
 // Joins the partial sums of 16 tokens: 64 threads a token each take every 64th strip in order, then
 // the 64 are joined in pairs.
@@ -222,7 +247,7 @@ GemmOp dx_op(const CeArgs &a, const E *dl, const E *w, int64_t piece, int64_t wi
 // workspace: dl of a piece, dx in 32 bits where there are several, the partial products of one product
 // at a time
 struct BwdLayout {
-    int64_t acc, part, total;
+    int64_t dl, acc, part, total;  // the two factors come first
 };
 template <typename E>
 BwdLayout bwd_layout(const CeArgs &a) {
@@ -235,7 +260,8 @@ BwdLayout bwd_layout(const CeArgs &a) {
         part = part > x ? part : x;
     }
     BwdLayout l;
-    l.acc = up256(a.N * piece * (int64_t)sizeof(E));
+    l.dl = 256;
+    l.acc = l.dl + up256(a.N * piece * (int64_t)sizeof(E));
     l.part = l.acc + (piece < a.V ? up256(a.N * a.D * 4) : 0);
     l.total = l.part + part;
     return l;
@@ -245,24 +271,28 @@ template <typename E>
 hipError_t bwd_t(const CeArgs &a, hipStream_t s) {
     const int64_t piece = piece_of(a.N, a.V);
     const BwdLayout l = bwd_layout<E>(a);
-    E *dl = (E *)a.ws;
+    float *scale = (float *)a.ws;
+    E *dl = (E *)((char *)a.ws + l.dl);
     float *acc = (float *)((char *)a.ws + l.acc);
     void *part = (char *)a.ws + l.part;
+    hipLaunchKernelGGL(ce_scale_kernel, dim3(1), dim3(1024), 0, s, a.dloss, a.t, a.N, a.V, scale);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
         const int64_t width = a.V - v0 < piece ? a.V - v0 : piece;
         const E *w = (const E *)a.w + v0 * a.D;
         const GemmOp gl{{a.x, nullptr}, {w, nullptr}, a.D, a.D, a.N, width, a.D};
-        hipError_t e = launch_gemm<E, true, true, 1>(
-            gl, GradEpi<E>{a.t, a.lse_in, a.dloss, dl, a.N, a.V, v0, width, piece}, s);
+        e = launch_gemm<E, true, true, 1>(
+            gl, GradEpi<E>{a.t, a.lse_in, a.dloss, scale + 1, dl, a.N, a.V, v0, width, piece}, s);
         if (e != hipSuccess) return e;
         e = launch_gemm_store<E, false, false>(
             dw_op(a, dl, piece, width),
-            StoreEpi<E>{{(E *)a.dw + v0 * a.D, nullptr}, nullptr, nullptr, nullptr, width, a.D, a.D}, part, s);
+            StoreEpi<E>{{(E *)a.dw + v0 * a.D, nullptr}, nullptr, nullptr, nullptr, scale, width, a.D, a.D}, part, s);
         if (e != hipSuccess) return e;
         const bool last = v0 + piece >= a.V;
         e = launch_gemm_store<E, true, false>(
             dx_op(a, dl, w, piece, width),
-            StoreEpi<E>{{last ? (E *)a.dx : nullptr, nullptr}, v0 ? acc : nullptr, acc, nullptr, a.N, a.D, a.D}, part, s);
+            StoreEpi<E>{{last ? (E *)a.dx : nullptr, nullptr}, v0 ? acc : nullptr, acc, nullptr, scale, a.N, a.D, a.D}, part, s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
