@@ -537,7 +537,7 @@ hipError_t launch_gemm_tile(TileGemmArgs a, const Epi &epi, hipStream_t s) {
 
 // ---------------------------------------------------------------- few rows
 
-// The product for at most 16 MT rows of A (a decode batch): B's rows, the weights, are read once, straight into
+// The product for a few rows of A (a decode batch), 16 MT of them a workgroup: B's rows, the weights, are read once, straight into
 // matrix operands, and that read is all it costs. A workgroup of eight waves owns 16 NT rows of each B: NT
 // tiles of 16, and KS = 8 / NT waves share a tile's k in turns of 128 bytes, so that a wave's loads
 // cover whole lines and enough of them are in flight (four turns a wave: 64 KB a workgroup, two workgroups a
@@ -558,7 +558,10 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void gemm_rows_kernel(TileGem
 #pragma unroll
     for (int b = 0; b < NB; ++b) w[b] = (const E *)a.B[b] + (n < a.N ? n : a.N - 1) * a.ldb + kl;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) x[i] = (const E *)a.A[0] + (16 * i + c < a.M ? 16 * i + c : a.M - 1) * a.lda + kl;
+    for (int i = 0; i < MT; ++i) {
+        const int64_t m = (int64_t)blockIdx.y * (16 * MT) + 16 * i + c;
+        x[i] = (const E *)a.A[0] + (m < a.M ? m : a.M - 1) * a.lda + kl;
+    }
     floatx4 acc[NB][MT];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -606,18 +609,16 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void gemm_rows_kernel(TileGem
 #pragma unroll
                 for (int k = 1; k < KS; ++k) sum[b][i][j] += held[k][j][b][i][lane];
             }
-    epi(sum, 0, n0, 0, nullptr);
+    epi(sum, (int64_t)blockIdx.y * (16 * MT), n0, 0, nullptr);
 }
 
 template <typename E, int NB, int MT, int NT, class Epi>
 hipError_t launch_gemm_rows(const TileGemmArgs &a, const Epi &epi, hipStream_t s) {
     const int64_t blocks = (a.N + 16 * NT - 1) / (16 * NT);
-    hipLaunchKernelGGL((gemm_rows_kernel<E, NB, MT, NT, Epi>), dim3((unsigned)blocks), dim3(512), 0, s, a, epi);
+    hipLaunchKernelGGL((gemm_rows_kernel<E, NB, MT, NT, Epi>), dim3((unsigned)blocks, (unsigned)((a.M + 16 * MT - 1) / (16 * MT))), dim3(512), 0,
+                       s, a, epi);
     return hipGetLastError();
 }
-
-// columns of C per partial sum of a wave (linear_ce.hip) in the tiled and in the any-size kernel
-constexpr int kTileCols = 64, kAnyCols = 32;
 
 // C = sum of A_p B_p^T in the order given by AKC and BKC (true: k contiguous, the leading dimension
 // between rows; false: rows contiguous, the leading dimension between k).
@@ -626,32 +627,91 @@ struct GemmOp {
     int64_t lda, ldb, M, N, K;
     int pairs = 1, batch = 1;  // at most one of them 2: A[0] B[0] + A[1] B[1], or the two side by side
     int slices = 1;            // of k: the epilogue gets partial products (batch x slices + slice)
+    int tile = 0;              // the tile to use; 0: chosen here
 };
+// columns of a wave's partial sum in the tiled and in the any-size kernel
+constexpr int kTileCols = 64, kAnyCols = 32;
 // whether rows of ld elements are whole 16-byte pieces
 template <typename E>
 bool whole_pieces(int64_t ld) {
     return ld * (int64_t)sizeof(E) % 16 == 0;
 }
-// The tile: 256 x 256 (one workgroup a compute unit) from 192 tiles on; below, 128 x 128 (two) while there
-// are 384 of them; below, 64 x 128 (three). Fewer, larger tiles read less and multiply faster, but
-// leave compute units idle: (feed-forward forward, 2048 x 8192) 256 tokens took 27.2 us in 256 tiles of
-// 128 x 128. fp32 products are bound by the matrix instructions at 128 x 128 already.
-inline int tile_of(int64_t M, int64_t N, int parts, bool bf16) {
-    if (bf16 && ((M + 255) / 256) * ((N + 255) / 256) * parts >= 192) return 256;
-    return ((M + 127) / 128) * ((N + 127) / 128) * parts >= 384 ? 128 : 64;
+// How a product is run. Tiles of 256 x 256 (bf16, one workgroup a compute unit), 128 x 128 or 64 x 128 (two); a
+// plain product's k may be cut into slices that are summed afterwards. The choice is the least of
+//   rounds (blocks a slice * block + fixed) + what summing the slices costs,
+// rounds = tiles * slices / resident workgroups, rounded up, with the times measured on this chip: a block of
+// 128 bytes of k with every compute unit busy 1.6, 1.05 and 0.8 us (fp32: 4.6 and 2.0 us, of which the matrix
+// instructions 3.6 and 1.8), a tile's start and stores 16, 5 and 3 us, a slice's 4 bytes at 3 TB/s and a
+// launch. What the model is for: 129 tiles of 256 x 256 are one round that leaves half the chip idle, 516 of 128 x
+// 128 are two of which one is empty (cross entropy dx of 10904 x 744 in 22,528 columns: 722 us so).
+struct Choice {
+    int tile, slices;
+};
+inline Choice choose(int64_t M, int64_t N, int64_t nkb, int products, bool bf16, bool cut) {
+    struct {
+        int tile, rows, cols, resident;
+        double block, fixed;
+    } const kinds[] = {{256, 256, 256, kComputeUnits, 1.6, 16.},
+                 {128, 128, 128, 2 * kComputeUnits, bf16 ? 1.05 : 4.6, 5.},
+                 {64, 64, 128, 2 * kComputeUnits, bf16 ? 0.8 : 2.0, 3.}};
+    Choice best{64, 1};
+    double least = -1.;
+    for (const auto &k : kinds) {
+        if (k.tile == 256 && !bf16) continue;
+        const int64_t tiles = ((M + k.rows - 1) / k.rows) * ((N + k.cols - 1) / k.cols) * products;
+        for (int64_t want = 1; want <= (cut ? 32 : 1); ++want) {
+            if (want > 1 && nkb < 4 * want) break;
+            const int64_t kper = (nkb + want - 1) / want, s = (nkb + kper - 1) / kper;  // no slice empty
+            const int64_t rounds = (tiles * s + k.resident - 1) / k.resident;
+            const double sum = s > 1 ? 5. + (double)(s * products * M * N) * 4e-6 / 3. : 0.;
+            const double time = rounds * (kper * k.block + k.fixed) + sum;
+            if (least < 0. || time < least) {
+                least = time;
+                best = Choice{k.tile, (int)s};
+            }
+        }
+    }
+    return best;
 }
+template <typename E>
+int64_t k_blocks(int64_t K) {
+    return (K * (int64_t)sizeof(E) + 127) / 128;
+}
+
+// Whether the product (both operands k contiguous, `cols` rows of all B matrices) goes by rows: up to 64 rows
+// the weights' read is all there is; up to 256 it still wins where 64 x 128 tiles would leave half of the
+// compute units idle (85 rows, 1600 x 2 x 1181 fp32: 64 us in 38 tiles).
+inline bool by_rows(int64_t M, int64_t cols) {
+    return M > 0 && (M <= 64 || (M <= 256 && ((M + 63) / 64) * ((cols + 127) / 128) < 128));
+}
+// Columns of C of a workgroup that goes by rows, over 16: with one B four tiles of 16 where there are plenty
+// (16 rows x 2048 x 65536: 74 us with four, 79 us with two, which leave more partial sums to join), else one.
+inline int rows_tiles(int64_t N, int NB) { return NB == 1 && N >= 64 * 512 ? 4 : 1; }
+
+// Columns of C of one wave's partial sum (linear_ce.hip) when launch_gemm runs M x N with one B.
+template <typename E>
+int64_t wave_cols(int64_t M, int64_t N, int64_t ld) {
+    if (!whole_pieces<E>(ld)) return kAnyCols;
+    return by_rows(M, N) ? 16 * rows_tiles(N, 1) : kTileCols;
+}
+
 template <typename E, bool AKC, bool BKC, int NB, class Epi>
 hipError_t launch_gemm(const GemmOp &o, const Epi &epi, hipStream_t s) {
     if (whole_pieces<E>(o.lda) && whole_pieces<E>(o.ldb) && o.K > 0) {
         const TileGemmArgs t{{o.A[0], o.A[1]}, {o.B[0], o.B[1]}, o.lda, o.ldb, o.M, o.N, o.K, o.pairs, o.batch, o.slices, 0, 0, 0};
-        if constexpr (AKC && BKC) {
-            // NT: 64 columns a workgroup with one B (a partial sum's width), 16 of each of two
-            constexpr int NT = NB == 1 ? 4 : 1;
-            if (o.M > 0 && o.M <= 16) return launch_gemm_rows<E, NB, 1, NT>(t, epi, s);
-            if (o.M > 0 && o.M <= 32) return launch_gemm_rows<E, NB, 2, NT>(t, epi, s);
-            if (o.M > 0 && o.M <= 64) return launch_gemm_rows<E, NB, 4, NT>(t, epi, s);
-        }
-        const int tile = tile_of(o.M, o.N * NB, o.batch * o.slices, sizeof(E) == 2);
+        if constexpr (AKC && BKC)
+            if (by_rows(o.M, o.N * NB)) {
+                if constexpr (NB == 1)
+                    if (rows_tiles(o.N, NB) == 4)
+                        return o.M <= 16   ? launch_gemm_rows<E, NB, 1, 4>(t, epi, s)
+                               : o.M <= 32 ? launch_gemm_rows<E, NB, 2, 4>(t, epi, s)
+                                           : launch_gemm_rows<E, NB, 4, 4>(t, epi, s);
+                return o.M <= 16   ? launch_gemm_rows<E, NB, 1, 1>(t, epi, s)
+                       : o.M <= 32 ? launch_gemm_rows<E, NB, 2, 1>(t, epi, s)
+                                   : launch_gemm_rows<E, NB, 4, 1>(t, epi, s);
+            }
+        const int parts = o.batch * o.slices;
+        const int tile = o.tile ? o.tile : choose(o.M, o.N * NB, o.pairs * k_blocks<E>(o.K), parts, sizeof(E) == 2, false).tile;
         if constexpr (sizeof(E) == 2)
             if (tile == 256) return launch_gemm_tile<E, AKC, BKC, NB, 256, 256, 2, 2, 2>(t, epi, s);
         if (tile == 128) return launch_gemm_tile<E, AKC, BKC, NB, 128, 128, 2, 2, 2>(t, epi, s);
@@ -788,47 +848,42 @@ __global__ __launch_bounds__(256) void gemm_sum_kernel(const float *part, int pa
     else *reinterpret_cast<floatx4 *>(acc_out + i) = v;
 }
 
-// Slices of k of a plain product (rows of N elements): where the tiles of 128 x 128 (256 x 256 in bf16) do not
-// fill the compute units, k is cut so that they do, into slices of at least eight blocks. Each
-// slice costs a write and a read of C in 32 bits. A sum of two products is cut at the seam first.
-// (Cross entropy, 1021 tokens x 1024, vocabulary 32003: dx is 64 tiles of 501 blocks, 388 us uncut.)
+// The tile and the slices of k of a plain product (rows of N elements); a sum of two products is cut at the
+// seam first. The same for the workspace's size and for the launch.
 template <typename E>
-int slices_of(int64_t lda, int64_t ldb, int64_t M, int64_t N, int64_t K, int products) {
-    if (!whole_pieces<E>(lda) || !whole_pieces<E>(ldb) || N % 4 || M < 1 || K < 1) return 1;
-    if (tile_of(M, N, products, sizeof(E) == 2) == 256) return 1;
-    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128) * products, nkb = (K * (int64_t)sizeof(E) + 127) / 128;
-    int64_t s = 512 / tiles;
-    if (s > nkb / 8) s = nkb / 8;
-    if (s > 32) s = 32;
-    if (s < 2) return 1;
-    const int64_t kper = (nkb + s - 1) / s;
-    return (int)((nkb + kper - 1) / kper);  // none of them empty
+Choice store_choice(const GemmOp &o) {
+    if (!whole_pieces<E>(o.lda) || !whole_pieces<E>(o.ldb) || o.M < 1 || o.K < 1) return Choice{0, 1};
+    const Choice whole = choose(o.M, o.N, o.pairs * k_blocks<E>(o.K), o.batch, sizeof(E) == 2, false);
+    if (o.N % 4) return whole;
+    const Choice cut = choose(o.M, o.N, k_blocks<E>(o.K), o.pairs * o.batch, sizeof(E) == 2, true);
+    return cut.slices > 1 ? cut : whole;
 }
 // bytes of partial products launch_gemm_store needs
 template <typename E>
 int64_t store_ws_bytes(const GemmOp &o) {
-    const int products = o.pairs * o.batch, s = slices_of<E>(o.lda, o.ldb, o.M, o.N, o.K, products);
-    return s > 1 ? s * products * o.M * o.N * 4 : 0;
+    const int64_t s = store_choice<E>(o).slices;
+    return s > 1 ? s * o.pairs * o.batch * o.M * o.N * 4 : 0;
 }
-// The plain product (epi.part is set here), cut where slices_of says so.
+// The plain product (epi.part is set here), cut where store_choice says so.
 template <typename E, bool AKC, bool BKC>
 hipError_t launch_gemm_store(const GemmOp &o, StoreEpi<E> epi, void *ws, hipStream_t s) {
     epi.part = nullptr;
-    const int products = o.pairs * o.batch, slices = slices_of<E>(o.lda, o.ldb, o.M, o.N, o.K, products);
-    if (slices == 1) return launch_gemm<E, AKC, BKC, 1>(o, epi, s);
+    const Choice how = store_choice<E>(o);
+    GemmOp run = o;
+    run.tile = how.tile;
+    if (how.slices == 1) return launch_gemm<E, AKC, BKC, 1>(run, epi, s);
     if (epi.ld != o.N) return hipErrorInvalidValue;
-    GemmOp cut = o;
-    cut.pairs = 1;
-    cut.batch = products;
-    cut.slices = slices;
+    run.pairs = 1;
+    run.batch = o.pairs * o.batch;
+    run.slices = how.slices;
     StoreEpi<E> to_part = epi;
     to_part.part = (float *)ws;
     to_part.acc_in = nullptr;
-    const hipError_t e = launch_gemm<E, AKC, BKC, 1>(cut, to_part, s);
+    const hipError_t e = launch_gemm<E, AKC, BKC, 1>(run, to_part, s);
     if (e != hipSuccess) return e;
     const int64_t n = o.M * o.N;
     hipLaunchKernelGGL((gemm_sum_kernel<E>), dim3((unsigned)((n / 4 + 255) / 256), (unsigned)o.batch), dim3(256), 0, s, (const float *)ws,
-                       slices * o.pairs, n, epi.out[0], epi.out[1], epi.acc_in, epi.acc_out, epi.scale);
+                       how.slices * o.pairs, n, epi.out[0], epi.out[1], epi.acc_in, epi.acc_out, epi.scale);
     return hipGetLastError();
 }
 

@@ -29,12 +29,6 @@ namespace {
 // exponential is 1 exactly.
 __device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
 
-// vocabulary columns per partial sum
-template <typename E>
-int64_t strip_of(int64_t D) {
-    return whole_pieces<E>(D) ? kTileCols : kAnyCols;
-}
-
 struct StatEpi {
     const int64_t *t;
     float2 *part;  // [strips][M]
@@ -208,9 +202,11 @@ __global__ __launch_bounds__(1024) void ce_join_kernel(const float2 *part, const
 }
 
 int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
+// partial sums of a token
 template <typename E>
-int64_t strips_of(int64_t D, int64_t V) {
-    return (V + strip_of<E>(D) - 1) / strip_of<E>(D);
+int64_t strips_of(int64_t N, int64_t D, int64_t V) {
+    const int64_t cols = wave_cols<E>(N, V, D);
+    return (V + cols - 1) / cols;
 }
 
 // Vocabulary columns per piece of the backward: dl of a piece takes at most about 512 MB.
@@ -224,7 +220,7 @@ int64_t piece_of(int64_t N, int64_t V) {
 template <typename E>
 hipError_t fwd_t(const CeArgs &a, hipStream_t s) {
     if (a.N == 0) return hipSuccess;
-    const int64_t strips = strips_of<E>(a.D, a.V);
+    const int64_t strips = strips_of<E>(a.N, a.D, a.V);
     float *tgt = (float *)a.ws;
     float2 *part = (float2 *)((char *)a.ws + up256(a.N * 4));
     const GemmOp g{{a.x, nullptr}, {a.w, nullptr}, a.D, a.D, a.N, a.V, a.D};
@@ -301,7 +297,7 @@ hipError_t bwd_t(const CeArgs &a, hipStream_t s) {
 }  // namespace
 
 int64_t ce_fwd_ws_bytes(int64_t N, int64_t D, int64_t V, int dtype) {
-    const int64_t strips = dtype == kDtypeBf16 ? strips_of<__bf16>(D, V) : strips_of<float>(D, V);
+    const int64_t strips = dtype == kDtypeBf16 ? strips_of<__bf16>(N, D, V) : strips_of<float>(N, D, V);
     return up256(N * 4) + strips * N * 8;
 }
 int64_t ce_bwd_ws_bytes(int64_t N, int64_t D, int64_t V, int dtype) {
