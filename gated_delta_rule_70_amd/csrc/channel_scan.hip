@@ -25,6 +25,13 @@
 // too: a first launch composes each chunk's map, and each workgroup of the second composes the
 // chunks before its own (behind it, in the backward) before it starts, at the cost of reading the
 // inputs of the maps twice.
+//
+// Measured (bf16): 4 x 4096 tokens x 2048 channels forward 72 us (268 MB, 3.7 TB/s), backward 127 us
+// (470 MB, 3.7 TB/s); the device's own large copy moves 4.9 TB/s. Per element the gates are 5
+// transcendental and about 25 other instructions, which at eight waves a compute unit nearly take the
+// time that the bytes take and do not all hide behind them. Split, 131,072 tokens x 1024 channels:
+// 219 us for the maps (805 MB, 3.7 TB/s) and 267 us for the scan (1074 MB, 4.0 TB/s). The chunks'
+// order is fixed, so the results do not depend on which workgroup comes first.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -568,7 +575,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, ScanP
 }
 
 // dA_log and ddt_bias: the units' sums [units][2][D], 16 slices of the units side by side and then
-// in order
+// in order. 4.6 us for 2048 channels, most of it the launch.
 __global__ __launch_bounds__(1024) void scan_param_kernel(const float *sums, int64_t units, int64_t D, float *dA, float *db) {
     __shared__ float held[2][16][64];
     const int lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
@@ -590,6 +597,8 @@ __global__ __launch_bounds__(1024) void scan_param_kernel(const float *sums, int
     }
 }
 
+// One token: a channel of a sequence a thread. Latency is all of it: 5.3 us as a launch for 256 x 4096
+// bf16 (16.8 MB, which the large copy's rate would move in 3.4).
 template <typename E>
 __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;

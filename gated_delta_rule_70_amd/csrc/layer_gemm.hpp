@@ -31,7 +31,9 @@ struct AnyGemmArgs {
 // Any sizes, strides and alignments: 64 x 64 tiles staged in LDS as fp32, fp32 matrix
 // instructions, every load checked. Four waves of 32 x 32. The sum over k is taken in blocks of
 // kSumK terms that are added up afterwards: one running fp32 sum over the 60,000 tokens of a weight
-// gradient was 2.1e-5 off (relative Frobenius), in blocks the error stops growing with the length.
+// gradient was 2.1e-5 off (relative Frobenius), in blocks the error stops growing with the length. Its
+// loads and LDS accesses are of single elements, which bounds it: 1021 x 2 x 2731 x 1023 fp32 takes 265 us (43 TFLOP/s), against 127 us in
+// gemm_tile_kernel for a width of 1024.
 constexpr int kAnyK = 16, kAnyLd = kAnyK + 1, kSumK = 512;
 template <typename E, int NB, class Epi>
 __global__ __launch_bounds__(256) void gemm_any_kernel(AnyGemmArgs a, Epi epi) {
@@ -122,6 +124,11 @@ hipError_t launch_gemm_any(const AnyGemmArgs &a, const Epi &epi, hipStream_t s) 
 // last are multiplied and its results are stored. Work is laid out so that the 32 or so tiles an XCD
 // runs at a time are neighbours (its L2 holds their operand rows): workgroup i runs on XCD i % 8 and
 // takes tiles from the i % 8 th contiguous eighth, in columns of eight tiles of m.
+//
+// Bound by the matrix instructions and their feeding: 1.2 to 1.28 PFLOP/s on the large bf16 products
+// (16384 x 16384 x 2048 and the like; the instruction alone, operands in registers, sustains 2.05; the
+// large tile holds one wave a SIMD, so what a wave waits for at a hand-over is not hidden), 92 TFLOP/s
+// on 1021 x 2731 x 1024 fp32, whose tiles do not fill the last round.
 struct TileGemmArgs {
     const void *A[2], *B[2];
     int64_t lda, ldb;
@@ -543,8 +550,9 @@ hipError_t launch_gemm_tile(TileGemmArgs a, const Epi &epi, hipStream_t s) {
 // cover whole lines and enough of them are in flight (four turns a wave: 64 KB a workgroup, two workgroups a
 // compute unit). The waves' sums are added in order through LDS and the first wave runs the epilogue. A's
 // rows come from L2 (rows past M repeat the last one; their columns are not stored). Both operands k
-// contiguous, rows whole 16-byte pieces. Feed-forward forward of one token, 2048 x 8192 (67 MB of weights):
-// 23.3 us with the tiled kernel.
+// contiguous, rows whole 16-byte pieces. Bound by that read: feed-forward forward of one token, 2048 x 8192
+// (67 MB of weights), 14.8 us (4.5 TB/s), 23.3 us with the tiled kernel; 16 tokens in 65,536 columns
+// of 2048 (268 MB) 67 us (4.0 TB/s).
 template <typename E, int NB, int MT, int NT, class Epi>
 __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void gemm_rows_kernel(TileGemmArgs a, Epi epi) {
     constexpr int KS = 8 / NT, es = sizeof(E), step = 64 / es, G = 4 / MT;  // step: k of one matrix step; G: turns in flight
@@ -834,7 +842,7 @@ struct StoreEpi {
 };
 
 // C[b] = (acc_in +) the sum of its `parts` partial products, in order; four neighbours a thread. n: elements
-// of one product, a multiple of 4.
+// of one product, a multiple of 4. Bound by memory: 6.8 us for 1021 x 1024 in eight slices (36 MB, 5.2 TB/s).
 template <typename E>
 __global__ __launch_bounds__(256) void gemm_sum_kernel(const float *part, int parts, int64_t n, E *out0, E *out1,
                                                        const float *acc_in, float *acc_out, const float *scale) {

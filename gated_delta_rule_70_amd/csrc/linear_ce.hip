@@ -11,6 +11,12 @@
 // partial sums of a token. Backward: for each piece of the vocabulary the logits are formed again
 // and turned into dl (in the inputs' type, as the operand of two products, its common factor apart), then
 // dW's rows of the piece are complete and dx is summed over the pieces in 32 bits.
+//
+// Matrix instructions bound it where there are many tokens: 16384 tokens, 2048 x 65536, bf16: forward
+// 3.67 ms (1199 TFLOP/s), backward 4 x (1.10 ms for dl, of which 0.1 its 537 MB of stores; 0.90 for dx;
+// 0.86 for dW: 999, 1216 and 1278 TFLOP/s). Keeping the logits instead of forming them again would take 2.1 GB
+// in bf16 and round them. With few tokens the read of W does: 16 tokens 74 us (268 MB, 3.6 TB/s with the
+// join's 7 us).
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <initializer_list>
@@ -29,6 +35,7 @@ namespace {
 // exponential is 1 exactly.
 __device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
 
+// The forward's epilogue: per token and strip of kTileCols columns (max, sum of e^{l - max}).
 struct StatEpi {
     const int64_t *t;
     float2 *part;  // [strips][M]
@@ -153,7 +160,8 @@ struct GradEpi {
 // The largest |dloss| of a token that bears a loss, and its inverse (1 and 1 where there is none). It is taken out of dl before
 // dl is rounded to the inputs' type and multiplied back into dx and dW, in 32 bits: with a mean over tokens
 // every dloss is the same number, whose rounding would be a common error of all of dl (2.9e-3 of dW in bf16
-// against 64 bits; without it the large entries, p - 1 at the targets, are near -1 and lose little).
+// against 64 bits; without it the large entries, p - 1 at the targets, are near -1 and lose little). One
+// workgroup: 15 us for 16384 tokens, next to 11 ms.
 __global__ __launch_bounds__(1024) void ce_scale_kernel(const float *dloss, const int64_t *t, int64_t N, int64_t V, float *scale) {
     __shared__ float held[16];
     float top = 0.f;
@@ -174,7 +182,7 @@ __global__ __launch_bounds__(1024) void ce_scale_kernel(const float *dloss, cons
 }
 
 // Joins the partial sums of 16 tokens: 64 threads a token each take every 64th strip in order, then
-// the 64 are joined in pairs.
+// the 64 are joined in pairs. 30 us for 16384 tokens x 1024 strips (134 MB, 4.5 TB/s), 7 us for 16 tokens.
 __global__ __launch_bounds__(1024) void ce_join_kernel(const float2 *part, const float *tgt, const int64_t *t, float *loss,
                                                        float *lse, int64_t N, int64_t V, int64_t strips) {
     __shared__ float2 held[64][16];
