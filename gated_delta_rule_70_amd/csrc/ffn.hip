@@ -49,6 +49,7 @@ struct GluEpi {
     E *h, *gate, *up;
     int64_t M, F;
     int act;
+    static constexpr bool whole = true;
     template <int MI, int NI>
     __device__ __forceinline__ void operator()(const floatx4 (&acc)[2][MI][NI], int64_t m0, int64_t n0, int, char *st) const {
 #pragma unroll

@@ -305,7 +305,7 @@ __device__ __forceinline__ void mma_step_agpr(floatx4 &acc, bf16x8 a, bf16x8 b) 
 }
 
 template <typename E, bool AKC, bool BKC, int NB, int BM, int BN, int WM, int WN, int S, class Epi>
-__global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 : 2) void gemm_tile_kernel(TileGemmArgs, Epi) {
+__global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 : WM * WN / 2) void gemm_tile_kernel(TileGemmArgs, Epi) {
     constexpr int NW = WM * WN, TM = BM / WM, TN = BN / NB / WN, MI = TM / 16, NI = TN / 16, KB = 128 / (int)sizeof(E);
     static_assert(NB == 1 || BKC, "two B matrices come k contiguous");
     __shared__ __align__(1024) char lds[S][(BM + BN) * 128];
@@ -648,19 +648,21 @@ bool whole_pieces(int64_t ld) {
 // plain product's k may be cut into slices that are summed afterwards. The choice is the least of
 //   rounds (blocks a slice * block + fixed) + what summing the slices costs,
 // rounds = tiles * slices / resident workgroups, rounded up, with the times measured on this chip: a block of
-// 128 bytes of k with every compute unit busy 1.6, 1.05 and 0.8 us (fp32: 4.6 and 2.0 us, of which the matrix
-// instructions 3.6 and 1.8), a tile's start and stores 16, 5 and 3 us, a slice's 4 bytes at 3 TB/s and a
-// launch. What the model is for: 129 tiles of 256 x 256 are one round that leaves half the chip idle, 516 of 128 x
+// 128 bytes of k with every compute unit busy 1.6, 1.1 and 0.8 us (fp32: 4.6 and 2.0 us, of which the matrix
+// instructions 3.6 and 1.8), a tile's start and end 24 (16 where the epilogue does not store the whole tile), 3.5
+// and 3 us, a slice's 4 bytes at 3 TB/s and a launch. The 128 x 128 tile has eight waves, so that one of a
+// SIMD's four multiplies while another stores: at 16 blocks of k (1021 x 32003 x 1024) its stored products take 91 us,
+// 105 with four waves and 103 in 256 x 256 tiles, at 32 and more the large tile wins. What the model is for: 129 tiles of 256 x 256 are one round that leaves half the chip idle, 516 of 128 x
 // 128 are two of which one is empty (cross entropy dx of 10904 x 744 in 22,528 columns: 722 us so).
 struct Choice {
     int tile, slices;
 };
-inline Choice choose(int64_t M, int64_t N, int64_t nkb, int products, bool bf16, bool cut) {
+inline Choice choose(int64_t M, int64_t N, int64_t nkb, int products, bool bf16, bool cut, bool whole) {
     struct {
         int tile, rows, cols, resident;
         double block, fixed;
-    } const kinds[] = {{256, 256, 256, kComputeUnits, 1.6, 16.},
-                 {128, 128, 128, 2 * kComputeUnits, bf16 ? 1.05 : 4.6, 5.},
+    } const kinds[] = {{256, 256, 256, kComputeUnits, 1.6, whole ? 24. : 16.},
+                 {128, 128, 128, 2 * kComputeUnits, bf16 ? 1.1 : 4.6, 3.5},
                  {64, 64, 128, 2 * kComputeUnits, bf16 ? 0.8 : 2.0, 3.}};
     Choice best{64, 1};
     double least = -1.;
@@ -719,10 +721,10 @@ hipError_t launch_gemm(const GemmOp &o, const Epi &epi, hipStream_t s) {
                                    : launch_gemm_rows<E, NB, 4, 1>(t, epi, s);
             }
         const int parts = o.batch * o.slices;
-        const int tile = o.tile ? o.tile : choose(o.M, o.N * NB, o.pairs * k_blocks<E>(o.K), parts, sizeof(E) == 2, false).tile;
+        const int tile = o.tile ? o.tile : choose(o.M, o.N * NB, o.pairs * k_blocks<E>(o.K), parts, sizeof(E) == 2, false, Epi::whole).tile;
         if constexpr (sizeof(E) == 2)
             if (tile == 256) return launch_gemm_tile<E, AKC, BKC, NB, 256, 256, 2, 2, 2>(t, epi, s);
-        if (tile == 128) return launch_gemm_tile<E, AKC, BKC, NB, 128, 128, 2, 2, 2>(t, epi, s);
+        if (tile == 128) return launch_gemm_tile<E, AKC, BKC, NB, 128, 128, 4, 2, 2>(t, epi, s);
         return launch_gemm_tile<E, AKC, BKC, NB, 64, 128, 2, 2, 3>(t, epi, s);
     }
     for (int b = 0; b < o.batch; ++b) {
@@ -811,6 +813,7 @@ struct StoreEpi {
     float *part;
     const float *scale;
     int64_t M, N, ld;
+    static constexpr bool whole = true;  // the epilogue stores the whole tile
     template <int MI, int NI>
     __device__ __forceinline__ void operator()(const floatx4 (&acc)[1][MI][NI], int64_t m0, int64_t n0, int z, char *st) const {
         const int lane = epilogue_lane(), g = lane >> 4, c = lane & 15;
@@ -861,9 +864,9 @@ __global__ __launch_bounds__(256) void gemm_sum_kernel(const float *part, int pa
 template <typename E>
 Choice store_choice(const GemmOp &o) {
     if (!whole_pieces<E>(o.lda) || !whole_pieces<E>(o.ldb) || o.M < 1 || o.K < 1) return Choice{0, 1};
-    const Choice whole = choose(o.M, o.N, o.pairs * k_blocks<E>(o.K), o.batch, sizeof(E) == 2, false);
+    const Choice whole = choose(o.M, o.N, o.pairs * k_blocks<E>(o.K), o.batch, sizeof(E) == 2, false, true);
     if (o.N % 4) return whole;
-    const Choice cut = choose(o.M, o.N, k_blocks<E>(o.K), o.pairs * o.batch, sizeof(E) == 2, true);
+    const Choice cut = choose(o.M, o.N, k_blocks<E>(o.K), o.pairs * o.batch, sizeof(E) == 2, true, true);
     return cut.slices > 1 ? cut : whole;
 }
 // bytes of partial products launch_gemm_store needs

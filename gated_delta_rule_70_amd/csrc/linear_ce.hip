@@ -41,6 +41,7 @@ struct StatEpi {
     float2 *part;  // [strips][M]
     float *tgt;    // [M]
     int64_t M, V;
+    static constexpr bool whole = false;
     template <int MI, int NI>
     __device__ __forceinline__ void operator()(const floatx4 (&acc)[1][MI][NI], int64_t m0, int64_t n0, int, char *st) const {
         constexpr int SJ = NI < kTileCols / 16 ? NI : kTileCols / 16, S = NI / SJ;  // tiles per strip, strips
@@ -112,6 +113,7 @@ struct GradEpi {
     const float *inv;  // 1 / the factor taken out of dl
     E *dl;
     int64_t M, V, v0, width, ld;
+    static constexpr bool whole = true;
     template <int MI, int NI>
     __device__ __forceinline__ void operator()(const floatx4 (&acc)[1][MI][NI], int64_t m0, int64_t n0, int, char *st) const {
         const int lane = epilogue_lane(), g = lane >> 4, c = lane & 15;
