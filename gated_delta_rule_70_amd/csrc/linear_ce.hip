@@ -219,10 +219,12 @@ int64_t strips_of(int64_t N, int64_t D, int64_t V) {
     return (V + cols - 1) / cols;
 }
 
-// Vocabulary columns per piece of the backward: dl of a piece takes at most about 512 MB.
+// Vocabulary columns per piece of the backward: dl of a piece takes at most about 512 MB, and its rows at most
+// 2^20 elements, as the other operands' (the products' offsets within a tile are 32 bits).
 int64_t piece_of(int64_t N, int64_t V) {
     int64_t p = (INT64_C(1) << 28) / (N > 0 ? N : 1) / 256 * 256;
     if (p < 2048) p = 2048;
+    if (p > INT64_C(1) << 20) p = INT64_C(1) << 20;
     const int64_t all = (V + 7) / 8 * 8;
     return p < all ? p : all;
 }

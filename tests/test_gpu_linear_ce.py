@@ -76,6 +76,12 @@ def test_several_pieces(gdr, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_pieces_of_few_tokens(gdr, dtype):
+    """Few tokens and a vocabulary past the longest row of a piece, 2^20."""
+    compare(gdr, 5, 16, 2 ** 20 + 1001, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_large_tiles_ragged(gdr, dtype):
     compare(gdr, 1100, 264, 3001, dtype)
 
