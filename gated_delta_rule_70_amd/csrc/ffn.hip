@@ -80,7 +80,8 @@ __global__ __launch_bounds__(256) void glu_grad_kernel(const E *gate, const E *u
     if (i >= M * pieces) return;
     const int64_t m = i / pieces, n = (i - m * pieces) * V, k = m * F + n;
     Piece g, u, d;
-    if (F % V == 0) {
+    // Whole pieces inside the row; ld may hold one more than F (fp32, F % 8 == 4), which is all zeros.
+    if (F % V == 0 && n < F) {
         g = *reinterpret_cast<const Piece *>(gate + k);
         u = *reinterpret_cast<const Piece *>(up + k);
         d = *reinterpret_cast<const Piece *>(dh + k);

@@ -174,3 +174,19 @@ def test_refusals(gdr):
         gdr.gated_ffn_bwd(x, wg, wu, dh.bfloat16(), dh, dh)
     with pytest.raises(gdr.GdrError, match="workspace"):
         gdr.gated_ffn_bwd(x, wg, wu, dh, dh.clone(), dh.clone(), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("F", [12, 500, 36, 16, 13])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_padding_of_the_gradients_rows(gdr, F, dtype):
+    """The backward's workspace begins with dG and dU, rows of F rounded up to 8 columns. The columns past F
+    hold zeros and nothing that lies behind a row of gate, up or dh; here each is the head of a larger
+    tensor of ones."""
+    M, D, ld = 5, 16, (F + 7) // 8 * 8
+    x, wg, wu, _ = (t.cuda() for t in make(M, D, F, dtype, 9))
+    heads = [torch.ones(M * F + 64, dtype=dtype, device="cuda")[: M * F].view(M, F) for _ in range(3)]
+    ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+    gdr.gated_ffn_bwd(x, wg, wu, *heads, workspace=ws)
+    kept = ws[: 2 * M * ld * x.element_size()].view(dtype).view(2, M, ld)
+    assert torch.isfinite(kept).all() and kept[:, :, :F].any()
+    assert not kept[:, :, F:].any()
