@@ -626,7 +626,7 @@ ScanPlan plan_of(int64_t T, int64_t D, int64_t nseq, bool packed, int vec) {
     p.units = nseq;
     p.per_seq = 1;
     const int64_t rows = packed ? T : nseq * T, blocks = (rows + kScanBlock - 1) / kScanBlock;
-    if (T <= kScanBlock || nseq * p.ntile >= (packed ? 1024 : 224)) return p;
+    if (nseq == 0 || T <= kScanBlock || nseq * p.ntile >= (packed ? 1024 : 224)) return p;
     const int64_t per = (blocks * p.ntile + 767) / 768;
     p.chunk = per * kScanBlock;
     p.per_seq = (T + p.chunk - 1) / p.chunk;

@@ -212,3 +212,13 @@ def test_long_scan_with_the_state_in_place(gdr, reverse):
     state = h.clone()
     out, same, _ = gdr.channel_scan_fwd(x, a, b, A, dt, state, cu, reverse=reverse, hT=state)
     assert same is state and torch.equal(out, want) and torch.equal(state, hT)
+
+
+@pytest.mark.parametrize("T", [1, 300, 5000])
+def test_empty_batch(gdr, T):
+    _, _, _, A, dt, _, _ = cuda(scan_case([4], 20, FP32, 230))
+    e = torch.empty(0, T, 20, device="cuda")
+    out, hT, states = gdr.channel_scan_fwd(e, e, e, A, dt, want_states=True)
+    assert out.shape == e.shape and hT.shape == (0, 20)
+    got = gdr.channel_scan_bwd(e, e, e, A, dt, states, e)
+    assert got[0].shape == e.shape and got[5].shape == (0, 20) and not got[3].any() and not got[4].any()

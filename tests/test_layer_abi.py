@@ -125,3 +125,12 @@ def test_sizes_of_buffers():
     for f in (lib.gdr_linear_ce_fwd_workspace_bytes, lib.gdr_linear_ce_bwd_workspace_bytes):
         assert f(ctypes.byref(binding.CeDims(1, 1, 0, 0, 0))) == -1
         assert f(ctypes.byref(binding.CeDims(100, 64, 5000, 1, 0))) > 0
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("T", [0, 1, 256, 257, 300, 100000])
+def test_sizes_of_an_empty_batch(T, dtype):
+    lib = binding.load()
+    d = binding.ScanDims(0, T, 20, 0, dtype, 0)
+    for f in (lib.gdr_channel_scan_states_elems, lib.gdr_channel_scan_fwd_workspace_bytes, lib.gdr_channel_scan_bwd_workspace_bytes):
+        assert f(ctypes.byref(d), 0) == 0
