@@ -473,7 +473,9 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, ScanP
                 if (MODE == kCompose) q[j][i].alpha = alpha_of((float)ga[j][i] + bias[i], rate[i]);
                 else q[j][i] = gates_of((float)ga[j][i], (float)gb[j][i], bias[i], rate[i]);
             }
-        if (left < kScanBlock) {  // past the end: the identity, with no gradient of its own
+        // Past the end: the identity, with no gradient of its own. x and the other gates are what the safe
+        // address holds, maybe another channel's NaN: they reach states past the end only, which nothing reads.
+        if (left < kScanBlock) {
 #pragma unroll
             for (int j = 0; j < kLen; ++j) {
                 const bool in = ln.has(j, left);
@@ -481,11 +483,6 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, ScanP
                 for (int i = 0; i < V; ++i) {
                     q[j][i].alpha = in ? q[j][i].alpha : 1.f;
                     go[j][i] = in ? go[j][i] : (E)0.f;
-                    if (MODE != kCompose) {
-                        q[j][i].beta = in ? q[j][i].beta : 0.f;
-                        q[j][i].la = in ? q[j][i].la : 0.f;
-                        q[j][i].rs = in ? q[j][i].rs : 0.f;
-                    }
                 }
             }
         }
@@ -526,20 +523,23 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, ScanP
         E *dx = (E *)a.dx + row, *da = (E *)a.da + row, *db = (E *)a.db + row;
 #pragma unroll
         for (int j = kLen - 1; j >= 0; --j) {
-            float vx[V], va[V], vb[V];
+            float vx[V], va[V], vb[V], dla[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const Gates &g = q[j][i];
                 const float up = (float)go[j][i] + c[i];
-                const float dla = g.alpha * prev[j][i] * up;
+                dla[i] = g.alpha * prev[j][i] * up;
                 vx[i] = g.beta * up;
-                va[i] = -g.rs * dla;
+                va[i] = -g.rs * dla[i];
                 vb[i] = vx[i] * (1.f - g.beta) * (float)x[j][i];
-                sA[i] = fmaf(dla, g.la, sA[i]);
-                sb[i] += va[i];
                 c[i] = g.alpha * up;
             }
             if (left == kScanBlock ? ln.on : ln.has(j, left)) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    sA[i] = fmaf(dla[i], q[j][i].la, sA[i]);
+                    sb[i] += va[i];
+                }
                 ln.store(dx, j, vx);
                 ln.store(da, j, va);
                 ln.store(db, j, vb);

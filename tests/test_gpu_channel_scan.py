@@ -222,3 +222,41 @@ def test_empty_batch(gdr, T):
     assert out.shape == e.shape and hT.shape == (0, 20)
     got = gdr.channel_scan_bwd(e, e, e, A, dt, states, e)
     assert got[0].shape == e.shape and got[5].shape == (0, 20) and not got[3].any() and not got[4].any()
+
+
+def train(gdr, x, a, b, A, dt, h, dout, reverse=False):
+    out, hT, states = gdr.channel_scan_fwd(x, a, b, A, dt, h, reverse=reverse, want_states=True)
+    return (out, hT) + gdr.channel_scan_bwd(x, a, b, A, dt, states, dout, reverse=reverse)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("T,D,B", [(3, 20, 1), (40, 64, 2), (300, 36, 1), (300, 4000, 2)])
+def test_a_bad_value_stays_in_its_channel(gdr, T, D, B, reverse, dtype):
+    """NaN or infinity in the inputs of one channel, at a token that ends or begins a sequence's ragged block:
+    every result of the other channels keeps its bits."""
+    x, a, b, A, dt, h, _ = cuda(scan_case([T] * B, D, dtype, 240 + T))
+    dout = upstream(x, B, 241)[0].cuda()
+    want = train(gdr, x, a, b, A, dt, h, dout, reverse)
+    for t in sorted({0, T - 1, T // 256 * 256 % T, (T - 1) % 256}):
+        for d in (0, 17):
+            for name, bad in (("x", "inf"), ("x", "nan"), ("a", "nan"), ("b", "nan"), ("dout", "nan")):
+                ins = dict(x=x, a=a, b=b, dout=dout)
+                ins[name] = ins[name].clone()
+                ins[name][0, t, d] = float(bad)
+                got = train(gdr, ins["x"], ins["a"], ins["b"], A, dt, h, ins["dout"], reverse)
+                keep = torch.arange(D) != d
+                for k, (p, q) in enumerate(zip(got, want)):
+                    assert torch.equal(p[..., keep], q[..., keep]), (t, d, name, bad, k)
+
+
+@pytest.mark.parametrize("T", [40, 256, 300])
+def test_an_infinite_last_input(gdr, T):
+    """The last token's input reaches no state that a token begins with: the gates' gradients stay finite."""
+    x, a, b, A, dt, h, _ = cuda(scan_case([T], 24, FP32, 250))
+    dout, dh = (t.cuda() for t in upstream(x, 1, 251))
+    x[0, T - 1, 3] = float("inf")
+    states = gdr.channel_scan_fwd(x, a, b, A, dt, h, want_states=True)[2]
+    dx, da, db, dA, ddt, dh0 = gdr.channel_scan_bwd(x, a, b, A, dt, states, dout, None, dh)
+    assert all(torch.isfinite(t).all() for t in (dx, da, dA, ddt, dh0))
+    assert torch.isinf(db[0, T - 1, 3]) and torch.isfinite(db[0, : T - 1]).all()
