@@ -70,8 +70,9 @@ __device__ __forceinline__ Gates gates_of(float a, float b, float bias, float ra
     const float u = a + bias;
     float z, w;
     Gates g;
-    // finite, so that la times a vanished alpha is 0
-    g.la = fmaxf(log2_alpha(u, rate, z, w), -1e30f);
+    // not -infinity, so that la times a vanished alpha is 0; a comparison, which lets NaN through
+    const float la = log2_alpha(u, rate, z, w);
+    g.la = la < -1e30f ? -1e30f : la;
     g.alpha = __builtin_amdgcn_exp2f(g.la);
     g.beta = sigmoid_of(b);
     g.rs = rate * (u >= 0.f ? 1.f : z) * __builtin_amdgcn_rcpf(w);

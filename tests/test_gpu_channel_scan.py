@@ -260,3 +260,24 @@ def test_an_infinite_last_input(gdr, T):
     dx, da, db, dA, ddt, dh0 = gdr.channel_scan_bwd(x, a, b, A, dt, states, dout, None, dh)
     assert all(torch.isfinite(t).all() for t in (dx, da, dA, ddt, dh0))
     assert torch.isinf(db[0, T - 1, 3]) and torch.isfinite(db[0, : T - 1]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("T,D,B", [(40, 20, 1), (700, 36, 1), (300, 4000, 2)])
+def test_a_nan_reaches_what_depends_on_it(gdr, T, D, B, reverse, dtype):
+    """NaN in each input of one channel in turn: the results that are not finite are the oracle's."""
+    x, a, b, A, dt, h, _ = scan_case([T] * B, D, dtype, 260 + T)
+    dout = upstream(x, B, 261)[0]
+    t, d = T // 2 + 3, 7
+    for name in ("x", "a", "b", "dout"):
+        say("channel scan NaN in %s, T %d D %d %s reverse %s" % (name, T, D, dtype, reverse))
+        ins = dict(x=x, a=a, b=b, dout=dout)
+        ins[name] = ins[name].clone()
+        ins[name][0, t, d] = float("nan")
+        got = train(gdr, *cuda((ins["x"], ins["a"], ins["b"], A, dt, h, ins["dout"])), reverse)
+        # the oracle on the channel with the NaN
+        one = [v[..., d : d + 1] for v in (ins["x"], ins["a"], ins["b"], A, dt, h)]
+        ref = L.scan(*one, None, reverse) + L.scan_grads(*one[:5], ins["dout"][..., d : d + 1], one[5], None, None, reverse)
+        for k, (p, q) in enumerate(zip(got, ref)):
+            assert np.array_equal(torch.isfinite(p[..., d : d + 1]).cpu().numpy(), np.isfinite(q)), (name, k)
