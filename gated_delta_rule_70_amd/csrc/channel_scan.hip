@@ -474,8 +474,8 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, ScanP
                 if (MODE == kCompose) q[j][i].alpha = alpha_of((float)ga[j][i] + bias[i], rate[i]);
                 else q[j][i] = gates_of((float)ga[j][i], (float)gb[j][i], bias[i], rate[i]);
             }
-        // Past the end: the identity, with no gradient of its own. x and the other gates are what the safe
-        // address holds, maybe another channel's NaN: they reach states past the end only, which nothing reads.
+        // Past the end: the identity, with no gradient of its own. x and beta are what the safe address
+        // holds, maybe another channel's NaN: they reach states past the end only.
         if (left < kScanBlock) {
 #pragma unroll
             for (int j = 0; j < kLen; ++j) {
@@ -484,6 +484,10 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, ScanP
                 for (int i = 0; i < V; ++i) {
                     q[j][i].alpha = in ? q[j][i].alpha : 1.f;
                     go[j][i] = in ? go[j][i] : (E)0.f;
+                    if (MODE != kCompose) {
+                        q[j][i].la = in ? q[j][i].la : 0.f;
+                        q[j][i].rs = in ? q[j][i].rs : 0.f;
+                    }
                 }
             }
         }
@@ -520,27 +524,30 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, ScanP
                 prev[j][i] = h[i];
                 h[i] = fmaf(q[j][i].alpha, h[i], q[j][i].beta * (float)x[j][i]);
             }
+        if (left < kScanBlock) {  // the states past the end, out of the sums
+#pragma unroll
+            for (int j = 0; j < kLen; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) prev[j][i] = ln.has(j, left) ? prev[j][i] : 0.f;
+        }
         const int64_t row = block_row(a, n, t) * a.D;
         E *dx = (E *)a.dx + row, *da = (E *)a.da + row, *db = (E *)a.db + row;
 #pragma unroll
         for (int j = kLen - 1; j >= 0; --j) {
-            float vx[V], va[V], vb[V], dla[V];
+            float vx[V], va[V], vb[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const Gates &g = q[j][i];
                 const float up = (float)go[j][i] + c[i];
-                dla[i] = g.alpha * prev[j][i] * up;
+                const float dla = g.alpha * prev[j][i] * up;
                 vx[i] = g.beta * up;
-                va[i] = -g.rs * dla[i];
+                va[i] = -g.rs * dla;
                 vb[i] = vx[i] * (1.f - g.beta) * (float)x[j][i];
+                sA[i] = fmaf(dla, g.la, sA[i]);
+                sb[i] += va[i];
                 c[i] = g.alpha * up;
             }
             if (left == kScanBlock ? ln.on : ln.has(j, left)) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    sA[i] = fmaf(dla[i], q[j][i].la, sA[i]);
-                    sb[i] += va[i];
-                }
                 ln.store(dx, j, vx);
                 ln.store(da, j, va);
                 ln.store(db, j, vb);
