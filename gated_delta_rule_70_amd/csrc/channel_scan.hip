@@ -63,8 +63,15 @@ __device__ __forceinline__ float alpha_of(float u, float rate) {
     float z, w;
     return __builtin_amdgcn_exp2f(log2_alpha(u, rate, z, w));
 }
+// The backward needs 1 - beta too, and to its own bits: by subtraction it is 1e-3 off at b = 10 and 0 from 17
+// on. One number holds both: the smaller of the two, with the sign bit set where that is 1 - beta.
 struct Gates {
-    float alpha, beta, la, rs;  // la = log2 alpha, rs = e^{A_log} sigmoid(u)
+    float alpha, sig, la, rs;  // la = log2 alpha, rs = e^{A_log} sigmoid(u)
+    __device__ __forceinline__ bool open() const { return __float_as_int(sig) < 0; }
+    __device__ __forceinline__ float beta() const { return open() ? 1.f + sig : sig; }
+    __device__ __forceinline__ float shut() const { return open() ? -sig : 1.f - sig; }  // 1 - beta
+    // computed anew from here on: what was derived is not kept through a phase of the block
+    __device__ __forceinline__ void forget() { asm("" : "+v"(sig)); }
 };
 __device__ __forceinline__ Gates gates_of(float a, float b, float bias, float rate) {
     const float u = a + bias;
@@ -74,7 +81,8 @@ __device__ __forceinline__ Gates gates_of(float a, float b, float bias, float ra
     const float la = log2_alpha(u, rate, z, w);
     g.la = la < -1e30f ? -1e30f : la;
     g.alpha = __builtin_amdgcn_exp2f(g.la);
-    g.beta = sigmoid_of(b);
+    const float e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(b)), s = e * __builtin_amdgcn_rcpf(1.f + e);
+    g.sig = b > 0.f ? -s : s;
     g.rs = rate * (u >= 0.f ? 1.f : z) * __builtin_amdgcn_rcpf(w);
     return g;
 }
@@ -495,7 +503,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, ScanP
         for (int j = 0; j < kLen; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                if (MODE != kCompose) H[i] = fmaf(q[j][i].alpha, H[i], q[j][i].beta * (float)x[j][i]);
+                if (MODE != kCompose) H[i] = fmaf(q[j][i].alpha, H[i], q[j][i].beta() * (float)x[j][i]);
                 P[i] *= q[j][i].alpha;
             }
 #pragma unroll
@@ -522,7 +530,8 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, ScanP
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 prev[j][i] = h[i];
-                h[i] = fmaf(q[j][i].alpha, h[i], q[j][i].beta * (float)x[j][i]);
+                q[j][i].forget();
+                h[i] = fmaf(q[j][i].alpha, h[i], q[j][i].beta() * (float)x[j][i]);
             }
         if (left < kScanBlock) {  // the states past the end, out of the sums
 #pragma unroll
@@ -537,12 +546,13 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, ScanP
             float vx[V], va[V], vb[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const Gates &g = q[j][i];
+                Gates &g = q[j][i];
+                g.forget();
                 const float up = (float)go[j][i] + c[i];
                 const float dla = g.alpha * prev[j][i] * up;
-                vx[i] = g.beta * up;
+                vx[i] = g.beta() * up;
                 va[i] = -g.rs * dla;
-                vb[i] = vx[i] * (1.f - g.beta) * (float)x[j][i];
+                vb[i] = vx[i] * g.shut() * (float)x[j][i];
                 sA[i] = fmaf(dla, g.la, sA[i]);
                 sb[i] += va[i];
                 c[i] = g.alpha * up;

@@ -281,3 +281,20 @@ def test_a_nan_reaches_what_depends_on_it(gdr, T, D, B, reverse, dtype):
         ref = L.scan(*one, None, reverse) + L.scan_grads(*one[:5], ins["dout"][..., d : d + 1], one[5], None, None, reverse)
         for k, (p, q) in enumerate(zip(got, ref)):
             assert np.array_equal(torch.isfinite(p[..., d : d + 1]).cpu().numpy(), np.isfinite(q)), (name, k)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("level", [-20.0, -10.0, -6.0, 6.0, 10.0, 14.0, 17.0, 25.0, 40.0])
+def test_gradient_of_open_and_shut_gates(gdr, level, dtype):
+    """db = beta (1 - beta) x g keeps its bits where beta is 1 but for a small part, which the 64-bit reference
+    forms as sigmoid(-b). The exponent's own rounding, 40 log2(e) 2^-24, is within the tolerances."""
+    x, a, b, A, dt, h, _ = scan_case([300], 24, dtype, 270)
+    b = torch.full_like(b, level)
+    dout, dh = upstream(x, 1, 271)
+    ref = L.scan_grads(x, a, b, A, dt, dout, h, None, dh)
+    db = ref[0] * L.f64(x) / (1.0 + np.exp(level))
+    gx, ga, gb, gA, gdt, gh, gdout, gdh = cuda((x, a, b, A, dt, h, dout, dh))
+    states = gdr.channel_scan_fwd(gx, ga, gb, gA, gdt, gh, want_states=True)[2]
+    got = gdr.channel_scan_bwd(gx, ga, gb, gA, gdt, states, gdout, None, gdh)
+    check(got[2], db, TOL[dtype], "db")
+    check(got[0], ref[0], TOL[dtype], "dx")
