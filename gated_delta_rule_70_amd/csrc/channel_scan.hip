@@ -282,15 +282,17 @@ enum ScanMode { kWhole, kCompose, kApply };
 
 // workgroup -> (unit, channel tile), the tiles of a unit side by side on one XCD: their rows share
 // 128-byte lines
-__device__ __forceinline__ int64_t xcd_order(int64_t all) {
-    const int64_t id = blockIdx.x, x = id & 7, q = all >> 3, r = all & 7;
+__device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t all) {
+    const int64_t x = id & 7, q = all >> 3, r = all & 7;
     return x * q + (x < r ? x : r) + (id >> 3);
 }
 
 template <typename E, int V, int MODE>
 __global__ __launch_bounds__(kThreads, 2) void scan_fwd_kernel(ScanArgs a, ScanPlan p, float2 *agg) {
     __shared__ WaveMap<V> rec[2][kWaves][16];
-    const int64_t w = xcd_order(p.units * p.ntile), u = w / p.ntile;
+    const int64_t all = p.units * p.ntile, id = block_id();
+    if (id >= all) return;
+    const int64_t w = xcd_order(id, all), u = w / p.ntile;
     const Unit n = unit_of(a, p, u);
     if (p.chunk && n.t0 >= n.len && n.c > 0) return;  // a slot without a chunk
     Lane<E, V> ln;
@@ -407,7 +409,9 @@ template <typename E, int V, int MODE>
 __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, ScanPlan p, float2 *agg, float *sums) {
     __shared__ WaveMap<V> rec[2][kWaves][16], rec_back[2][kWaves][16];
     __shared__ float part[2][V][kSlots][16];
-    const int64_t w = xcd_order(p.units * p.ntile), u = w / p.ntile;
+    const int64_t all = p.units * p.ntile, id = block_id();
+    if (id >= all) return;
+    const int64_t w = xcd_order(id, all), u = w / p.ntile;
     const Unit n = unit_of(a, p, u);
     Lane<E, V> ln;
     ln.init(a, w % p.ntile);
@@ -619,7 +623,7 @@ __global__ __launch_bounds__(1024) void scan_param_kernel(const float *sums, int
 // bf16 (16.8 MB, which the large copy's rate would move in 3.4).
 template <typename E>
 __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = block_id() * 256 + threadIdx.x;
     if (i >= a.nseq * a.D) return;
     const int64_t d = i % a.D;
     const float alpha = alpha_of((float)((const E *)a.a)[i] + a.dt_bias[d], expf(a.A_log[d]));
@@ -656,7 +660,7 @@ ScanPlan plan_of(const ScanArgs &a, int vec) { return plan_of(a.T, a.D, a.nseq, 
 template <typename E, int V>
 hipError_t fwd_t(const ScanArgs &a, hipStream_t s) {
     const ScanPlan p = plan_of(a, V);
-    const dim3 grid((unsigned)(p.units * p.ntile)), block(kThreads);
+    const dim3 grid = grid_of(p.units * p.ntile, kThreads), block(kThreads);
     float2 *agg = (float2 *)a.ws;
     if (!p.chunk) {
         hipLaunchKernelGGL((scan_fwd_kernel<E, V, kWhole>), grid, block, 0, s, a, p, agg);
@@ -672,7 +676,7 @@ hipError_t fwd_t(const ScanArgs &a, hipStream_t s) {
 template <typename E, int V>
 hipError_t bwd_t(const ScanArgs &a, hipStream_t s) {
     const ScanPlan p = plan_of(a, V);
-    const dim3 grid((unsigned)(p.units * p.ntile)), block(kThreads);
+    const dim3 grid = grid_of(p.units * p.ntile, kThreads), block(kThreads);
     float *sums = a.ws;
     float2 *agg = (float2 *)(a.ws + 2 * p.units * a.D);
     if (a.nseq > 0) {
@@ -717,7 +721,7 @@ hipError_t launch_scan_bwd(const ScanArgs &a, int dtype, hipStream_t s) {
 hipError_t launch_scan_step(const ScanArgs &a, int dtype, hipStream_t s) {
     const int64_t n = a.nseq * a.D;
     if (n == 0) return hipSuccess;
-    const dim3 grid((unsigned)((n + 255) / 256)), block(256);
+    const dim3 grid = grid_of((n + 255) / 256, 256), block(256);
     if (dtype == kDtypeBf16) hipLaunchKernelGGL((scan_step_kernel<__bf16>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((scan_step_kernel<float>), grid, block, 0, s, a);
     return hipGetLastError();

@@ -76,7 +76,7 @@ __global__ __launch_bounds__(256) void glu_grad_kernel(const E *gate, const E *u
                                                        int64_t F, int64_t ld, int act) {
     constexpr int V = 16 / sizeof(E);
     typedef E Piece __attribute__((ext_vector_type(V)));
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, pieces = ld / V;
+    const int64_t i = block_id() * 256 + threadIdx.x, pieces = ld / V;
     if (i >= M * pieces) return;
     const int64_t m = i / pieces, n = (i - m * pieces) * V, k = m * F + n;
     Piece g, u, d;
@@ -139,7 +139,7 @@ hipError_t bwd_t(const FfnArgs &a, hipStream_t s) {
     void *part = du + a.M * ld;
     if (a.M > 0) {
         const int64_t blocks = (a.M * ld / (16 / (int64_t)sizeof(E)) + 255) / 256;
-        hipLaunchKernelGGL((glu_grad_kernel<E>), dim3((unsigned)blocks), dim3(256), 0, s, (const E *)a.gate,
+        hipLaunchKernelGGL((glu_grad_kernel<E>), grid_of(blocks, 256), dim3(256), 0, s, (const E *)a.gate,
                            (const E *)a.up, (const E *)a.dh, dg, du, a.M, a.F, ld, a.act);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;

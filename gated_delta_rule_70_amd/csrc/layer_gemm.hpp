@@ -13,6 +13,7 @@
 #include <stdint.h>
 
 #include "gdr_mfma.hpp"
+#include "layer_kernels.hpp"
 
 // a lambda of a kernel, whose captures have to stay in registers
 #define GDR_INLINE __attribute__((always_inline))
@@ -39,8 +40,8 @@ template <typename E, int NB, class Epi>
 __global__ __launch_bounds__(256) void gemm_any_kernel(AnyGemmArgs a, Epi epi) {
     __shared__ float As[64 * kAnyLd], Bs[NB][64 * kAnyLd];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
-    const int64_t nm = (a.M + 63) / 64;
-    const int64_t m0 = (blockIdx.x % nm) * 64, n0 = (blockIdx.x / nm) * 64;
+    const int64_t nm = (a.M + 63) / 64, id = block_id(), m0 = (id % nm) * 64, n0 = (id / nm) * 64;
+    if (n0 >= a.N) return;
     const int wm = (wave & 1) * 32, wn = (wave >> 1) * 32;
     floatx4 acc[NB][2][2], total[NB][2][2];
     auto each = [&](auto f) {
@@ -91,7 +92,7 @@ hipError_t launch_gemm_any(const AnyGemmArgs &a, const Epi &epi, hipStream_t s) 
     const int64_t blocks = ((a.M + 63) / 64) * ((a.N + 63) / 64);
     if (blocks == 0) return hipSuccess;
     if (blocks > INT32_MAX) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((gemm_any_kernel<E, NB, Epi>), dim3((unsigned)blocks), dim3(256), 0, s, a, epi);
+    hipLaunchKernelGGL((gemm_any_kernel<E, NB, Epi>), grid_of(blocks, 256), dim3(256), 0, s, a, epi);
     return hipGetLastError();
 }
 
@@ -528,7 +529,7 @@ hipError_t launch_gemm_tile(TileGemmArgs a, const Epi &epi, hipStream_t s) {
     const int64_t nm = (a.M + BM - 1) / BM, nn = (a.N + BN / NB - 1) / (BN / NB);
     if (nm * nn == 0) return hipSuccess;
     const int64_t all = nm * nn * a.batch * a.slices, nkb = (a.K * (int64_t)sizeof(E) + 127) / 128;
-    if (all > INT32_MAX / 16 || a.K < 1 || a.pairs * a.batch * NB > 2 || a.pairs * a.batch < 1 || nkb > INT32_MAX / 4 ||
+    if (all > INT32_MAX / 2 || a.K < 1 || a.pairs * a.batch * NB > 2 || a.pairs * a.batch < 1 || nkb > INT32_MAX / 4 ||
         a.slices < 1 || (a.pairs > 1 && a.slices > 1))
         return hipErrorInvalidValue;
     // slices of whole blocks, none of them empty
@@ -560,14 +561,15 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void gemm_rows_kernel(TileGem
     __shared__ floatx4 held[KS][NT][NB][MT][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
     const int nt = wave % NT, ks = wave / NT;
-    const int64_t n0 = (int64_t)blockIdx.x * (16 * NT), n = n0 + 16 * nt + c;
+    const int64_t n0 = block_id() * (16 * NT), n = n0 + 16 * nt + c;
+    if (n0 >= a.N) return;
     const int kl = g * (16 / es);  // this lane's first k of a step
     const E *w[NB], *x[MT];
 #pragma unroll
     for (int b = 0; b < NB; ++b) w[b] = (const E *)a.B[b] + (n < a.N ? n : a.N - 1) * a.ldb + kl;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-        const int64_t m = (int64_t)blockIdx.y * (16 * MT) + 16 * i + c;
+        const int64_t m = (int64_t)blockIdx.z * (16 * MT) + 16 * i + c;
         x[i] = (const E *)a.A[0] + (m < a.M ? m : a.M - 1) * a.lda + kl;
     }
     floatx4 acc[NB][MT];
@@ -617,14 +619,15 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void gemm_rows_kernel(TileGem
 #pragma unroll
                 for (int k = 1; k < KS; ++k) sum[b][i][j] += held[k][j][b][i][lane];
             }
-    epi(sum, (int64_t)blockIdx.y * (16 * MT), n0, 0, nullptr);
+    epi(sum, (int64_t)blockIdx.z * (16 * MT), n0, 0, nullptr);
 }
 
 template <typename E, int NB, int MT, int NT, class Epi>
 hipError_t launch_gemm_rows(const TileGemmArgs &a, const Epi &epi, hipStream_t s) {
     const int64_t blocks = (a.N + 16 * NT - 1) / (16 * NT);
-    hipLaunchKernelGGL((gemm_rows_kernel<E, NB, MT, NT, Epi>), dim3((unsigned)blocks, (unsigned)((a.M + 16 * MT - 1) / (16 * MT))), dim3(512), 0,
-                       s, a, epi);
+    dim3 grid = grid_of(blocks, 512);
+    grid.z = (unsigned)((a.M + 16 * MT - 1) / (16 * MT));
+    hipLaunchKernelGGL((gemm_rows_kernel<E, NB, MT, NT, Epi>), grid, dim3(512), 0, s, a, epi);
     return hipGetLastError();
 }
 

@@ -12,6 +12,14 @@ namespace gdr {
 // cu[s] / kScanBlock + s, so that no two sequences share one.
 constexpr int kScanBlock = 256;
 
+// A launch takes fewer than 2^32 threads along x: more workgroups go along y as well. A kernel numbers
+// them with block_id(), and those past its last one have nothing to do.
+inline dim3 grid_of(int64_t blocks, int threads) {
+    const int64_t most = INT64_C(0xffffffff) / threads, rows = (blocks + most - 1) / most;
+    return rows < 2 ? dim3((unsigned)blocks) : dim3((unsigned)((blocks + rows - 1) / rows), (unsigned)rows);
+}
+__device__ __forceinline__ int64_t block_id() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 struct ScanArgs {
     const void *x, *a, *b;          // [B][T][D]
     const float *A_log, *dt_bias;   // [D]

@@ -189,7 +189,7 @@ __global__ __launch_bounds__(1024) void ce_join_kernel(const float2 *part, const
                                                        float *lse, int64_t N, int64_t V, int64_t strips) {
     __shared__ float2 held[64][16];
     const int c = threadIdx.x & 15, slot = threadIdx.x >> 4;
-    const int64_t n = (int64_t)blockIdx.x * 16 + c;
+    const int64_t n = block_id() * 16 + c;
     auto join = [](float2 p, float2 q) {
         const float m = fmaxf(p.x, q.x), ref = m == -INFINITY ? 0.f : m;
         return make_float2(m, p.y * expf(p.x - ref) + q.y * expf(q.x - ref));
@@ -238,7 +238,7 @@ hipError_t fwd_t(const CeArgs &a, hipStream_t s) {
     const GemmOp g{{a.x, nullptr}, {a.w, nullptr}, a.D, a.D, a.N, a.V, a.D};
     const hipError_t e = launch_gemm<E, true, true, 1>(g, StatEpi{a.t, part, tgt, a.N, a.V}, s);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(ce_join_kernel, dim3((unsigned)((a.N + 15) / 16)), dim3(1024), 0, s, part, tgt, a.t, a.loss, a.lse,
+    hipLaunchKernelGGL(ce_join_kernel, grid_of((a.N + 15) / 16, 1024), dim3(1024), 0, s, part, tgt, a.t, a.loss, a.lse,
                        a.N, a.V, strips);
     return hipGetLastError();
 }
