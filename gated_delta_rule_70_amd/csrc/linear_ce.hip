@@ -159,13 +159,40 @@ struct GradEpi {
     }
 };
 
-// The largest |dloss| of a token that bears a loss, and its inverse (1 and 1 where there is none). It is taken out of dl before
-// dl is rounded to the inputs' type and multiplied back into dx and dW, in 32 bits: with a mean over tokens
-// every dloss is the same number, whose rounding would be a common error of all of dl (2.9e-3 of dW in bf16
-// against 64 bits; without it the large entries, p - 1 at the targets, are near -1 and lose little). One
-// workgroup: 15 us for 16384 tokens, next to 11 ms.
-__global__ __launch_bounds__(1024) void ce_scale_kernel(const float *dloss, const int64_t *t, int64_t N, int64_t V, float *scale) {
+// What the backward's products need of the tokens, in one launch.
+// Workgroup 0: the largest |dloss| of a token that bears a loss, and its inverse (1 and 1 where there is none). It is
+// taken out of dl before dl is rounded to the inputs' type and multiplied back into dx and dW, in 32 bits: with a
+// mean over tokens every dloss is the same number, whose rounding would be a common error of all of dl (2.9e-3 of dW
+// in bf16 against 64 bits; without it the large entries, p - 1 at the targets, are near -1 and lose little).
+// The others: a copy of x for dW = dl^T x, with zeros in the rows of the tokens without a loss. Their dl is 0, but
+// 0 times what a padded row may hold, NaN or infinity, would be in all of dW.
+template <typename E>
+__global__ __launch_bounds__(1024) void ce_tokens_kernel(const float *dloss, const int64_t *t, const E *x, int64_t N, int64_t D,
+                                                         int64_t V, float *scale, E *kept) {
     __shared__ float held[16];
+    const int64_t id = block_id();
+    if (id > 0) {
+        constexpr int W = 16 / sizeof(E);
+        typedef E Piece __attribute__((ext_vector_type(W)));
+        const int64_t first = ((id - 1) * 4096 + threadIdx.x) * W;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t i = first + k * 1024 * W;
+            if (D % W == 0) {
+                if (i >= N * D) return;
+                const int64_t v = t[i / D];
+                Piece p = *reinterpret_cast<const Piece *>(x + i);
+                if (v < 0 || v >= V) p = Piece{};
+                *reinterpret_cast<Piece *>(kept + i) = p;
+            } else {
+                for (int64_t j = i; j < i + W && j < N * D; ++j) {
+                    const int64_t v = t[j / D];
+                    kept[j] = v < 0 || v >= V ? (E)0.f : x[j];
+                }
+            }
+        }
+        return;
+    }
     float top = 0.f;
 #pragma unroll 4
     for (int64_t n = threadIdx.x; n < N; n += 1024)
@@ -245,17 +272,17 @@ hipError_t fwd_t(const CeArgs &a, hipStream_t s) {
 
 // the products of one piece of the backward (`width` columns from w)
 template <typename E>
-GemmOp dw_op(const CeArgs &a, const E *dl, int64_t piece, int64_t width) {
-    return GemmOp{{dl, nullptr}, {a.x, nullptr}, piece, a.D, width, a.D, a.N};
+GemmOp dw_op(const CeArgs &a, const E *dl, const E *x, int64_t piece, int64_t width) {
+    return GemmOp{{dl, nullptr}, {x, nullptr}, piece, a.D, width, a.D, a.N};
 }
 template <typename E>
 GemmOp dx_op(const CeArgs &a, const E *dl, const E *w, int64_t piece, int64_t width) {
     return GemmOp{{dl, nullptr}, {w, nullptr}, piece, a.D, a.N, a.D, width};
 }
-// workspace: dl of a piece, dx in 32 bits where there are several, the partial products of one product
-// at a time
+// workspace: the two factors, x without the rows of tokens without a loss, dl of a piece, dx in 32 bits where
+// there are several, the partial products of one product at a time
 struct BwdLayout {
-    int64_t dl, acc, part, total;  // the two factors come first
+    int64_t x, dl, acc, part, total;
 };
 template <typename E>
 BwdLayout bwd_layout(const CeArgs &a) {
@@ -263,12 +290,13 @@ BwdLayout bwd_layout(const CeArgs &a) {
     const E *none = nullptr;
     int64_t part = 0;
     for (int64_t width : {piece < a.V ? piece : a.V, tail}) {
-        const int64_t w = store_ws_bytes<E>(dw_op(a, none, piece, width)), x = store_ws_bytes<E>(dx_op(a, none, none, piece, width));
+        const int64_t w = store_ws_bytes<E>(dw_op(a, none, none, piece, width)), x = store_ws_bytes<E>(dx_op(a, none, none, piece, width));
         part = part > w ? part : w;
         part = part > x ? part : x;
     }
     BwdLayout l;
-    l.dl = 256;
+    l.x = 256;
+    l.dl = l.x + up256(a.N * a.D * (int64_t)sizeof(E));
     l.acc = l.dl + up256(a.N * piece * (int64_t)sizeof(E));
     l.part = l.acc + (piece < a.V ? up256(a.N * a.D * 4) : 0);
     l.total = l.part + part;
@@ -280,10 +308,12 @@ hipError_t bwd_t(const CeArgs &a, hipStream_t s) {
     const int64_t piece = piece_of(a.N, a.V);
     const BwdLayout l = bwd_layout<E>(a);
     float *scale = (float *)a.ws;
-    E *dl = (E *)((char *)a.ws + l.dl);
+    E *x = (E *)((char *)a.ws + l.x), *dl = (E *)((char *)a.ws + l.dl);
     float *acc = (float *)((char *)a.ws + l.acc);
     void *part = (char *)a.ws + l.part;
-    hipLaunchKernelGGL(ce_scale_kernel, dim3(1), dim3(1024), 0, s, a.dloss, a.t, a.N, a.V, scale);
+    const int64_t copied = 4096 * (16 / (int64_t)sizeof(E));  // elements of x a workgroup
+    hipLaunchKernelGGL((ce_tokens_kernel<E>), grid_of(1 + (a.N * a.D + copied - 1) / copied, 1024), dim3(1024), 0, s, a.dloss, a.t,
+                       (const E *)a.x, a.N, a.D, a.V, scale, x);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
@@ -294,7 +324,7 @@ hipError_t bwd_t(const CeArgs &a, hipStream_t s) {
             gl, GradEpi<E>{a.t, a.lse_in, a.dloss, scale + 1, dl, a.N, a.V, v0, width, piece}, s);
         if (e != hipSuccess) return e;
         e = launch_gemm_store<E, false, false>(
-            dw_op(a, dl, piece, width),
+            dw_op(a, dl, x, piece, width),
             StoreEpi<E>{{(E *)a.dw + v0 * a.D, nullptr}, nullptr, nullptr, nullptr, scale, width, a.D, a.D}, part, s);
         if (e != hipSuccess) return e;
         const bool last = v0 + piece >= a.V;

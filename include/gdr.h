@@ -566,8 +566,8 @@ typedef struct gdr_ce_dims {
  *
  *   x [N][D], w [V][D] dtype;  targets [N] int64 (DEVICE); loss, lse [N] fp32
  *
- * A token whose target is outside 0 .. V-1 bears no loss (0) and no gradient; its lse is written
- * all the same. The logits stay in fp32 and are reduced to a partial sum per token as they are
+ * A token whose target is outside 0 .. V-1 bears no loss (0) and no gradient, whatever its row of x
+ * holds (NaN and infinity too); its lse is written all the same. The logits stay in fp32 and are reduced to a partial sum per token as they are
  * formed.
  *
  * gdr_linear_ce_bwd - gradients of sum(loss * dloss): dx [N][D] and dw [V][D] in dtype, from lse as

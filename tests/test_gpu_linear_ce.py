@@ -194,3 +194,23 @@ def test_refusals(gdr):
         gdr.linear_ce_bwd(x, w, t, dl[:3], dl)
     with pytest.raises(gdr.GdrError, match="workspace"):
         gdr.linear_ce_bwd(x, w, t, dl, dl.clone(), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("N,D,V", [(1, 16, 40), (6, 64, 333), (7, 13, 50), (300, 64, 333), (520, 100, 2000), (60001, 8, 4801)])
+def test_rows_without_a_loss_may_hold_anything(gdr, N, D, V, dtype):
+    """NaN and infinity in x where the target is outside the vocabulary: no loss, and no gradient of the weights or
+    of any token, to the bit."""
+    x, w, t, dl = make(N, D, V, dtype, 12)
+    t[:: 3] = -100
+    gx, gw, gt, gdl = (v.cuda() for v in (x, w, t, dl))
+    off = (gt < 0) | (gt >= V)
+    loss, lse = gdr.linear_ce_fwd(gx, gw, gt)
+    want = gdr.linear_ce_bwd(gx, gw, gt, lse, gdl)
+    for value in ("nan", "inf"):
+        bad = gx.clone()
+        bad[off] = float(value)
+        got, lse2 = gdr.linear_ce_fwd(bad, gw, gt)
+        assert torch.equal(got, loss) and torch.equal(lse2[~off], lse[~off])
+        bdl = torch.where(off, torch.full_like(gdl, float(value)), gdl)
+        assert all(torch.equal(p, q) for p, q in zip(gdr.linear_ce_bwd(bad, gw, gt, lse2, bdl), want))
