@@ -38,7 +38,8 @@ __device__ __forceinline__ float act_f(float x, int act) {
 // the value and the derivative
 __device__ __forceinline__ void act_grad_f(float x, int act, float &val, float &der) {
     const float s = act == 0 ? x : 2.f * kGeluC * (x + kGeluA * x * x * x);
-    const float ds = act == 0 ? 1.f : 2.f * kGeluC * (1.f + 3.f * kGeluA * x * x);
+    // q (1 - q) vanishes long before |x| is 1e3; x^2 stays finite for it
+    const float y = __builtin_amdgcn_fmed3f(x, -1e3f, 1e3f), ds = act == 0 ? 1.f : 2.f * kGeluC * (1.f + 3.f * kGeluA * y * y);
     const float q = sigmoid_f(s);
     val = x * q;
     der = q + x * q * (1.f - q) * ds;

@@ -190,3 +190,20 @@ def test_padding_of_the_gradients_rows(gdr, F, dtype):
     kept = ws[: 2 * M * ld * x.element_size()].view(dtype).view(2, M, ld)
     assert torch.isfinite(kept).all() and kept[:, :, :F].any()
     assert not kept[:, :, F:].any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_slope_of_huge_gates(gdr, act, dtype):
+    """Past a few tens the activation is nearly 0 or the identity, its slope 0 or 1, up to the type's largest
+    values: each element within the backward's tolerance of the 64-bit one, or of 1."""
+    v = torch.tensor([50.0, 1e3, 2e4, 3e13, 3e19, 1e30, 3e38])
+    gate = torch.cat([v, -v]).to(dtype).cuda()[None]
+    F = gate.shape[1]
+    up, dh = torch.ones_like(gate), torch.ones_like(gate)
+    x, w = torch.ones(1, 8, dtype=dtype, device="cuda"), torch.zeros(F, 8, dtype=dtype, device="cuda")
+    dx, dwg, dwu = gdr.gated_ffn_bwd(x, w, w, gate, up, dh, act=act)
+    val, slope = L.act_and_slope(L.f64(gate[0]), act)
+    assert not dx.any()
+    for got, ref in ((dwg, slope), (dwu, val)):
+        assert (abs(L.f64(got) - ref[:, None]) <= BWD[dtype] * (1.0 + abs(ref[:, None]))).all()
