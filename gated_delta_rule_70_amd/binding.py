@@ -657,6 +657,8 @@ def _scan_args(x, a, b, A_log, dt_bias, cu_seqlens, reverse):
     S = B
     if cu_seqlens is not None:
         _need(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+            raise ValueError("cu_seqlens must have shape (S + 1,), S >= 1 (got %s)" % (tuple(cu_seqlens.shape),))
         S = cu_seqlens.shape[0] - 1
     return ScanDims(B, T, D, S if cu_seqlens is not None else 0, code, GDR_REVERSE if reverse else 0), S, dev
 
@@ -753,6 +755,8 @@ def _ffn_args(x, w_gate, w_up, act):
     _need(x, "x")
     dev, dt = x.device, x.dtype
     code = _dtype_code(dt, "x, w_gate, w_up")
+    if type(w_gate) is not torch.Tensor:
+        _need(w_gate, "w_gate")
     if x.dim() < 1 or w_gate.dim() != 2:
         raise ValueError("x must have shape (..., D) and w_gate (F, D) (got %s, %s)" % (tuple(x.shape), tuple(w_gate.shape)))
     if act not in ACTS:
@@ -803,6 +807,8 @@ def _ce_args(x, weight, targets):
     _need(x, "x")
     dev, dt = x.device, x.dtype
     code = _dtype_code(dt, "x, weight")
+    if type(weight) is not torch.Tensor:
+        _need(weight, "weight")
     if x.dim() != 2 or weight.dim() != 2:
         raise ValueError("x must have shape (N, D) and weight (V, D) (got %s, %s)" % (tuple(x.shape), tuple(weight.shape)))
     N, D = x.shape
