@@ -90,15 +90,6 @@ __device__ __forceinline__ Gates gates_of(float a, float b, float bias, float ra
 constexpr int kThreads = 512, kWaves = kThreads / 64, kSlots = 4 * kWaves, kLen = kScanBlock / kSlots;
 static_assert(kLen * kSlots == kScanBlock, "block shape");
 
-// How a launch walks the sequences: whole, or in chunks of `chunk` tokens. Packed chunks of sequence
-// s begin at slot cu[s] / chunk + s.
-struct ScanPlan {
-    int64_t chunk;   // 0: not split
-    int64_t units;   // sequences, or chunk slots
-    int64_t ntile;   // channel tiles
-    int64_t per_seq; // chunks of a sequence (not packed)
-};
-
 // One unit: tokens [t0, t1) of a sequence in scan order.
 struct Unit {
     int64_t s, row0, len, slot0;  // sequence, its first row, its tokens, its first block slot
@@ -632,30 +623,8 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a) {
     ((E *)a.out)[i] = (E)h;
 }
 
-// Channels a thread: 64-byte runs of a row for 16 lanes, as two bf16 a lane or one fp32 (two fp32, a third of
-// whose backward's registers spilled: 0.214 ms against 0.142 ms on packed fp32 sequences of 520 channels);
-// one bf16 where rows are not whole pairs.
-int vec_of(int64_t D, int dtype) { return dtype == kDtypeBf16 && D % 2 == 0 ? 2 : 1; }
-
-// Split where whole sequences would leave compute units idle: fewer than 224 workgroups (of 256), or,
-// packed, fewer than 1024 (their lengths differ and are not known here). Chunks are whole blocks, of a
-// size that gives about 768 workgroups: three a compute unit, which evens out the ends.
-ScanPlan plan_of(int64_t T, int64_t D, int64_t nseq, bool packed, int vec) {
-    ScanPlan p;
-    const int64_t cols = 16 * vec;
-    p.ntile = (D + cols - 1) / cols;
-    p.chunk = 0;
-    p.units = nseq;
-    p.per_seq = 1;
-    const int64_t rows = packed ? T : nseq * T, blocks = (rows + kScanBlock - 1) / kScanBlock;
-    if (nseq == 0 || T <= kScanBlock || nseq * p.ntile >= (packed ? 1024 : 224)) return p;
-    const int64_t per = (blocks * p.ntile + 767) / 768;
-    p.chunk = per * kScanBlock;
-    p.per_seq = (T + p.chunk - 1) / p.chunk;
-    p.units = packed ? T / p.chunk + nseq + 1 : nseq * p.per_seq;
-    return p;
-}
-ScanPlan plan_of(const ScanArgs &a, int vec) { return plan_of(a.T, a.D, a.nseq, a.cu_seqlens != nullptr, vec); }
+int vec_of(int64_t D, int dtype) { return scan_vec(D, dtype == kDtypeBf16 ? 2 : 4); }
+ScanPlan plan_of(const ScanArgs &a, int vec) { return scan_plan(a.T, a.D, a.nseq, a.cu_seqlens != nullptr, vec); }
 
 template <typename E, int V>
 hipError_t fwd_t(const ScanArgs &a, hipStream_t s) {
@@ -699,11 +668,11 @@ hipError_t bwd_t(const ScanArgs &a, hipStream_t s) {
 }  // namespace
 
 int64_t scan_fwd_ws_bytes(int64_t T, int64_t D, int64_t nseq, bool packed, int dtype) {
-    const ScanPlan p = plan_of(T, D, nseq, packed, vec_of(D, dtype));
+    const ScanPlan p = scan_plan(T, D, nseq, packed, vec_of(D, dtype));
     return p.chunk ? p.units * D * 8 : 0;
 }
 int64_t scan_bwd_ws_bytes(int64_t T, int64_t D, int64_t nseq, bool packed, int dtype) {
-    const ScanPlan p = plan_of(T, D, nseq, packed, vec_of(D, dtype));
+    const ScanPlan p = scan_plan(T, D, nseq, packed, vec_of(D, dtype));
     return p.units * D * (p.chunk ? 16 : 8);
 }
 

@@ -108,22 +108,28 @@ __global__ __launch_bounds__(256) void glu_grad_kernel(const E *gate, const E *u
     *reinterpret_cast<Piece *>(du + i * V) = pu;
 }
 
-int64_t grad_ld(int64_t F) { return (F + 7) / 8 * 8; }
-
 template <typename E>
 hipError_t fwd_t(const FfnArgs &a, hipStream_t s) {
-    const GemmOp g{{a.x, nullptr}, {a.wg, a.wu}, a.D, a.D, a.M, a.F, a.D};
+    GemmOp g = ffn_fwd_product(a.M, a.D, a.F);
+    g.A[0] = a.x;
+    g.B[0] = a.wg, g.B[1] = a.wu;
     return launch_gemm<E, true, true, 2>(g, GluEpi<E>{(E *)a.h, (E *)a.gate, (E *)a.up, a.M, a.F, a.act}, s);
 }
 
 // the products of the backward: dx, and both weights' gradients side by side
 template <typename E>
 GemmOp dx_op(const FfnArgs &a, const E *dg, const E *du) {
-    return GemmOp{{dg, du}, {a.wg, a.wu}, grad_ld(a.F), a.D, a.M, a.D, a.F, 2, 1};
+    GemmOp g = ffn_dx_product(a.M, a.D, a.F);
+    g.A[0] = dg, g.A[1] = du;
+    g.B[0] = a.wg, g.B[1] = a.wu;
+    return g;
 }
 template <typename E>
 GemmOp dw_op(const FfnArgs &a, const E *dg, const E *du) {
-    return GemmOp{{dg, du}, {a.x, a.x}, grad_ld(a.F), a.D, a.F, a.D, a.M, 1, 2};
+    GemmOp g = ffn_dw_product(a.M, a.D, a.F);
+    g.A[0] = dg, g.A[1] = du;
+    g.B[0] = g.B[1] = a.x;
+    return g;
 }
 // workspace: dG and dU, then the partial products of one product at a time
 template <typename E>

@@ -140,7 +140,6 @@ struct TileGemmArgs {
     int kper;
     int nm, nn;  // tiles
 };
-constexpr int kComputeUnits = 256;
 // LDS of one wave for 16 rows of results on their way to memory (RowStore)
 constexpr int stage_bytes(int MI) { return 16 * ((MI == 8 ? 256 : MI == 4 ? 128 : 64) + 16); }
 
@@ -631,103 +630,27 @@ hipError_t launch_gemm_rows(const TileGemmArgs &a, const Epi &epi, hipStream_t s
     return hipGetLastError();
 }
 
-// C = sum of A_p B_p^T in the order given by AKC and BKC (true: k contiguous, the leading dimension
-// between rows; false: rows contiguous, the leading dimension between k).
-struct GemmOp {
-    const void *A[2], *B[2];
-    int64_t lda, ldb, M, N, K;
-    int pairs = 1, batch = 1;  // at most one of them 2: A[0] B[0] + A[1] B[1], or the two side by side
-    int slices = 1;            // of k: the epilogue gets partial products (batch x slices + slice)
-    int tile = 0;              // the tile to use; 0: chosen here
-};
-// columns of a wave's partial sum in the tiled and in the any-size kernel
-constexpr int kTileCols = 64, kAnyCols = 32;
-// whether rows of ld elements are whole 16-byte pieces
-template <typename E>
-bool whole_pieces(int64_t ld) {
-    return ld * (int64_t)sizeof(E) % 16 == 0;
-}
-// How a product is run. Tiles of 256 x 256 (bf16, one workgroup a compute unit), 128 x 128 or 64 x 128 (two); a
-// plain product's k may be cut into slices that are summed afterwards. The choice is the least of
-//   rounds (blocks a slice * block + fixed) + what summing the slices costs,
-// rounds = tiles * slices / resident workgroups, rounded up, with the times measured on this chip: a block of
-// 128 bytes of k with every compute unit busy 1.6, 1.1 and 0.8 us (fp32: 4.6 and 2.0 us, of which the matrix
-// instructions 3.6 and 1.8), a tile's start and end 24 (16 where the epilogue does not store the whole tile), 3.5
-// and 3 us, a slice's 4 bytes at 3 TB/s and a launch. The 128 x 128 tile has eight waves, so that one of a
-// SIMD's four multiplies while another stores: at 16 blocks of k (1021 x 32003 x 1024) its stored products take 91 us,
-// 105 with four waves and 103 in 256 x 256 tiles, at 32 and more the large tile wins. What the model is for: 129 tiles of 256 x 256 are one round that leaves half the chip idle, 516 of 128 x
-// 128 are two of which one is empty (cross entropy dx of 10904 x 744 in 22,528 columns: 722 us so).
-struct Choice {
-    int tile, slices;
-};
-inline Choice choose(int64_t M, int64_t N, int64_t nkb, int products, bool bf16, bool cut, bool whole) {
-    struct {
-        int tile, rows, cols, resident;
-        double block, fixed;
-    } const kinds[] = {{256, 256, 256, kComputeUnits, 1.6, whole ? 24. : 16.},
-                 {128, 128, 128, 2 * kComputeUnits, bf16 ? 1.1 : 4.6, 3.5},
-                 {64, 64, 128, 2 * kComputeUnits, bf16 ? 0.8 : 2.0, 3.}};
-    Choice best{64, 1};
-    double least = -1.;
-    for (const auto &k : kinds) {
-        if (k.tile == 256 && !bf16) continue;
-        const int64_t tiles = ((M + k.rows - 1) / k.rows) * ((N + k.cols - 1) / k.cols) * products;
-        for (int64_t want = 1; want <= (cut ? 32 : 1); ++want) {
-            if (want > 1 && nkb < 4 * want) break;
-            const int64_t kper = (nkb + want - 1) / want, s = (nkb + kper - 1) / kper;  // no slice empty
-            const int64_t rounds = (tiles * s + k.resident - 1) / k.resident;
-            const double sum = s > 1 ? 5. + (double)(s * products * M * N) * 4e-6 / 3. : 0.;
-            const double time = rounds * (kper * k.block + k.fixed) + sum;
-            if (least < 0. || time < least) {
-                least = time;
-                best = Choice{k.tile, (int)s};
-            }
-        }
-    }
-    return best;
-}
-template <typename E>
-int64_t k_blocks(int64_t K) {
-    return (K * (int64_t)sizeof(E) + 127) / 128;
-}
-
-// Whether the product (both operands k contiguous, `cols` rows of all B matrices) goes by rows: up to 64 rows
-// the weights' read is all there is; up to 256 it still wins where 64 x 128 tiles would leave half of the
-// compute units idle (85 rows, 1600 x 2 x 1181 fp32: 64 us in 38 tiles).
-inline bool by_rows(int64_t M, int64_t cols) {
-    return M > 0 && (M <= 64 || (M <= 256 && ((M + 63) / 64) * ((cols + 127) / 128) < 128));
-}
-// Columns of C of a workgroup that goes by rows, over 16: with one B four tiles of 16 where there are plenty
-// (16 rows x 2048 x 65536: 74 us with four, 79 us with two, which leave more partial sums to join), else one.
-inline int rows_tiles(int64_t N, int NB) { return NB == 1 && N >= 64 * 512 ? 4 : 1; }
-
-// Columns of C of one wave's partial sum (linear_ce.hip) when launch_gemm runs M x N with one B.
-template <typename E>
-int64_t wave_cols(int64_t M, int64_t N, int64_t ld) {
-    if (!whole_pieces<E>(ld)) return kAnyCols;
-    return by_rows(M, N) ? 16 * rows_tiles(N, 1) : kTileCols;
-}
-
+// The product in the order given by AKC and BKC (true: k contiguous, the leading dimension between rows; false:
+// rows contiguous, the leading dimension between k), on the kernel that path_of names.
 template <typename E, bool AKC, bool BKC, int NB, class Epi>
 hipError_t launch_gemm(const GemmOp &o, const Epi &epi, hipStream_t s) {
-    if (whole_pieces<E>(o.lda) && whole_pieces<E>(o.ldb) && o.K > 0) {
+    const Path how = path_of(o, sizeof(E), NB, AKC && BKC, Epi::whole);
+    if (how.kind != Path::kAny) {
         const TileGemmArgs t{{o.A[0], o.A[1]}, {o.B[0], o.B[1]}, o.lda, o.ldb, o.M, o.N, o.K, o.pairs, o.batch, o.slices, 0, 0, 0};
         if constexpr (AKC && BKC)
-            if (by_rows(o.M, o.N * NB)) {
+            if (how.kind == Path::kRows) {
                 if constexpr (NB == 1)
-                    if (rows_tiles(o.N, NB) == 4)
-                        return o.M <= 16   ? launch_gemm_rows<E, NB, 1, 4>(t, epi, s)
-                               : o.M <= 32 ? launch_gemm_rows<E, NB, 2, 4>(t, epi, s)
-                                           : launch_gemm_rows<E, NB, 4, 4>(t, epi, s);
-                return o.M <= 16   ? launch_gemm_rows<E, NB, 1, 1>(t, epi, s)
-                       : o.M <= 32 ? launch_gemm_rows<E, NB, 2, 1>(t, epi, s)
-                                   : launch_gemm_rows<E, NB, 4, 1>(t, epi, s);
+                    if (how.nt == 4)
+                        return how.mt == 1   ? launch_gemm_rows<E, NB, 1, 4>(t, epi, s)
+                               : how.mt == 2 ? launch_gemm_rows<E, NB, 2, 4>(t, epi, s)
+                                             : launch_gemm_rows<E, NB, 4, 4>(t, epi, s);
+                return how.mt == 1   ? launch_gemm_rows<E, NB, 1, 1>(t, epi, s)
+                       : how.mt == 2 ? launch_gemm_rows<E, NB, 2, 1>(t, epi, s)
+                                     : launch_gemm_rows<E, NB, 4, 1>(t, epi, s);
             }
-        const int parts = o.batch * o.slices;
-        const int tile = o.tile ? o.tile : choose(o.M, o.N * NB, o.pairs * k_blocks<E>(o.K), parts, sizeof(E) == 2, false, Epi::whole).tile;
         if constexpr (sizeof(E) == 2)
-            if (tile == 256) return launch_gemm_tile<E, AKC, BKC, NB, 256, 256, 2, 2, 2>(t, epi, s);
-        if (tile == 128) return launch_gemm_tile<E, AKC, BKC, NB, 128, 128, 4, 2, 2>(t, epi, s);
+            if (how.tile == 256) return launch_gemm_tile<E, AKC, BKC, NB, 256, 256, 2, 2, 2>(t, epi, s);
+        if (how.tile == 128) return launch_gemm_tile<E, AKC, BKC, NB, 128, 128, 4, 2, 2>(t, epi, s);
         return launch_gemm_tile<E, AKC, BKC, NB, 64, 128, 2, 2, 3>(t, epi, s);
     }
     for (int b = 0; b < o.batch; ++b) {
@@ -862,27 +785,17 @@ __global__ __launch_bounds__(256) void gemm_sum_kernel(const float *part, int pa
     else *reinterpret_cast<floatx4 *>(acc_out + i) = v;
 }
 
-// The tile and the slices of k of a plain product (rows of N elements); a sum of two products is cut at the
-// seam first. The same for the workspace's size and for the launch.
-template <typename E>
-Choice store_choice(const GemmOp &o) {
-    if (!whole_pieces<E>(o.lda) || !whole_pieces<E>(o.ldb) || o.M < 1 || o.K < 1) return Choice{0, 1};
-    const Choice whole = choose(o.M, o.N, o.pairs * k_blocks<E>(o.K), o.batch, sizeof(E) == 2, false, true);
-    if (o.N % 4) return whole;
-    const Choice cut = choose(o.M, o.N, k_blocks<E>(o.K), o.pairs * o.batch, sizeof(E) == 2, true, true);
-    return cut.slices > 1 ? cut : whole;
-}
 // bytes of partial products launch_gemm_store needs
 template <typename E>
 int64_t store_ws_bytes(const GemmOp &o) {
-    const int64_t s = store_choice<E>(o).slices;
+    const int64_t s = store_choice(o, sizeof(E)).slices;
     return s > 1 ? s * o.pairs * o.batch * o.M * o.N * 4 : 0;
 }
 // The plain product (epi.part is set here), cut where store_choice says so.
 template <typename E, bool AKC, bool BKC>
 hipError_t launch_gemm_store(const GemmOp &o, StoreEpi<E> epi, void *ws, hipStream_t s) {
     epi.part = nullptr;
-    const Choice how = store_choice<E>(o);
+    const Choice how = store_choice(o, sizeof(E));
     GemmOp run = o;
     run.tile = how.tile;
     if (how.slices == 1) return launch_gemm<E, AKC, BKC, 1>(run, epi, s);

@@ -5,12 +5,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-namespace gdr {
+#include "layer_plan.hpp"
 
-// Tokens per block of the channel scan: the forward keeps the state that enters each block of a
-// sequence when the backward will run. Packed sequences: the blocks of sequence s start at slot
-// cu[s] / kScanBlock + s, so that no two sequences share one.
-constexpr int kScanBlock = 256;
+namespace gdr {
 
 // A launch takes fewer than 2^32 threads along x: more workgroups go along y as well. A kernel numbers
 // them with block_id(), and those past its last one have nothing to do.

@@ -242,18 +242,8 @@ int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
 // partial sums of a token
 template <typename E>
 int64_t strips_of(int64_t N, int64_t D, int64_t V) {
-    const int64_t cols = wave_cols<E>(N, V, D);
+    const int64_t cols = wave_cols(N, V, D, sizeof(E));
     return (V + cols - 1) / cols;
-}
-
-// Vocabulary columns per piece of the backward: dl of a piece takes at most about 512 MB, and its rows at most
-// 2^20 elements, as the other operands' (the products' offsets within a tile are 32 bits).
-int64_t piece_of(int64_t N, int64_t V) {
-    int64_t p = (INT64_C(1) << 28) / (N > 0 ? N : 1) / 256 * 256;
-    if (p < 2048) p = 2048;
-    if (p > INT64_C(1) << 20) p = INT64_C(1) << 20;
-    const int64_t all = (V + 7) / 8 * 8;
-    return p < all ? p : all;
 }
 
 template <typename E>
@@ -262,7 +252,9 @@ hipError_t fwd_t(const CeArgs &a, hipStream_t s) {
     const int64_t strips = strips_of<E>(a.N, a.D, a.V);
     float *tgt = (float *)a.ws;
     float2 *part = (float2 *)((char *)a.ws + up256(a.N * 4));
-    const GemmOp g{{a.x, nullptr}, {a.w, nullptr}, a.D, a.D, a.N, a.V, a.D};
+    GemmOp g = ce_logits_product(a.N, a.D, a.V);
+    g.A[0] = a.x;
+    g.B[0] = a.w;
     const hipError_t e = launch_gemm<E, true, true, 1>(g, StatEpi{a.t, part, tgt, a.N, a.V}, s);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(ce_join_kernel, grid_of((a.N + 15) / 16, 1024), dim3(1024), 0, s, part, tgt, a.t, a.loss, a.lse,
@@ -273,11 +265,17 @@ hipError_t fwd_t(const CeArgs &a, hipStream_t s) {
 // the products of one piece of the backward (`width` columns from w)
 template <typename E>
 GemmOp dw_op(const CeArgs &a, const E *dl, const E *x, int64_t piece, int64_t width) {
-    return GemmOp{{dl, nullptr}, {x, nullptr}, piece, a.D, width, a.D, a.N};
+    GemmOp g = ce_dw_product(a.N, a.D, piece, width);
+    g.A[0] = dl;
+    g.B[0] = x;
+    return g;
 }
 template <typename E>
 GemmOp dx_op(const CeArgs &a, const E *dl, const E *w, int64_t piece, int64_t width) {
-    return GemmOp{{dl, nullptr}, {w, nullptr}, piece, a.D, a.N, a.D, width};
+    GemmOp g = ce_dx_product(a.N, a.D, piece, width);
+    g.A[0] = dl;
+    g.B[0] = w;
+    return g;
 }
 // workspace: the two factors, x without the rows of tokens without a loss, dl of a piece, dx in 32 bits where
 // there are several, the partial products of one product at a time
@@ -286,7 +284,7 @@ struct BwdLayout {
 };
 template <typename E>
 BwdLayout bwd_layout(const CeArgs &a) {
-    const int64_t piece = piece_of(a.N, a.V), tail = a.V % piece ? a.V % piece : piece;
+    const int64_t piece = ce_piece(a.N, a.V), tail = a.V % piece ? a.V % piece : piece;
     const E *none = nullptr;
     int64_t part = 0;
     for (int64_t width : {piece < a.V ? piece : a.V, tail}) {
@@ -305,7 +303,7 @@ BwdLayout bwd_layout(const CeArgs &a) {
 
 template <typename E>
 hipError_t bwd_t(const CeArgs &a, hipStream_t s) {
-    const int64_t piece = piece_of(a.N, a.V);
+    const int64_t piece = ce_piece(a.N, a.V);
     const BwdLayout l = bwd_layout<E>(a);
     float *scale = (float *)a.ws;
     E *x = (E *)((char *)a.ws + l.x), *dl = (E *)((char *)a.ws + l.dl);
@@ -319,7 +317,9 @@ hipError_t bwd_t(const CeArgs &a, hipStream_t s) {
     for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
         const int64_t width = a.V - v0 < piece ? a.V - v0 : piece;
         const E *w = (const E *)a.w + v0 * a.D;
-        const GemmOp gl{{a.x, nullptr}, {w, nullptr}, a.D, a.D, a.N, width, a.D};
+        GemmOp gl = ce_logits_product(a.N, a.D, width);
+        gl.A[0] = a.x;
+        gl.B[0] = w;
         e = launch_gemm<E, true, true, 1>(
             gl, GradEpi<E>{a.t, a.lse_in, a.dloss, scale + 1, dl, a.N, a.V, v0, width, piece}, s);
         if (e != hipSuccess) return e;
