@@ -423,6 +423,10 @@ __global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 
                 for (int j = 0; j < NI; ++j) f(acc[b][i][j], total[blocked ? b : 0][blocked ? i : 0][blocked ? j : 0]);
     };
 
+    // What is on one side of this stays there: a wait between two of them separates the accumulators' writers from
+    // their readers, which nothing else holds to their places around an instruction in assembly.
+    auto held = [&]() GDR_INLINE { each([](floatx4 &p, floatx4 &) GDR_INLINE { asm volatile("" : "+a"(p)); }); };
+
     // fragments of the two halves of a block
     typename Fragments<E, AKC, BM, MI>::type va[2][MI], vb[2][NB * NI];
     // reads i0 .. i1 - 1 of the NB NI + MI of half ks of the block in slot h
@@ -479,8 +483,9 @@ __global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 
             if constexpr (blocked) t = zero4();
         });
         if constexpr (in_agprs) {  // written before the matrix instructions in assembly read them
-            each([](floatx4 &p, floatx4 &) GDR_INLINE { asm volatile("" : "+a"(p)); });
+            held();
             asm volatile("s_nop 7");
+            held();
         }
         int tm, tn, tz;
         locate(tile, tm, tn, tz);
@@ -504,8 +509,9 @@ __global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 
         if constexpr (blocked) each([](floatx4 &p, floatx4 &t) GDR_INLINE { p += t; });
         // matrix results are read by other instructions from here on: 18 wait states
         if constexpr (in_agprs) {
-            each([](floatx4 &p, floatx4 &) GDR_INLINE { asm volatile("" : "+a"(p)); });
+            held();
             asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+            held();
         }
         Epi epi;
         {
