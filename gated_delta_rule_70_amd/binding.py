@@ -749,6 +749,7 @@ def channel_scan_step(x, a, b, A_log, dt_bias, state_in, state_out=None, out=Non
 
 
 ACTS = {"silu": 0, "gelu_tanh": 1}
+GDR_FFN_KEEP_F32 = 256
 
 
 def _ffn_args(x, w_gate, w_up, act):
@@ -770,31 +771,45 @@ def _ffn_args(x, w_gate, w_up, act):
     return FfnDims(M, D, F, code, ACTS[act]), dev
 
 
-def gated_ffn_fwd(x, w_gate, w_up, *, act: str = "silu", out=None, want_saved: bool = False):
+def _keep(dims, dt, xdt, name):
+    """Marks in which dtype gate and up are kept."""
+    if dt == torch.float32:
+        dims.act |= GDR_FFN_KEEP_F32
+    elif dt != xdt:
+        raise ValueError("%s must be torch.float32 or %s (got %s)" % (name, xdt, dt))
+
+
+def gated_ffn_fwd(x, w_gate, w_up, *, act: str = "silu", out=None, want_saved: bool = False, saved_dtype=torch.float32):
     """Both projections of a gated feed-forward block, the activation and the product
     (``gdr_gated_ffn_fwd``): h = act(x w_gate^T) * (x w_up^T). x [..., D]; w_gate, w_up [F, D] (bf16
     or fp32, one dtype). Returns (h [..., F], gate, up); the projections gate and up [..., F] are kept
-    for ``gated_ffn_bwd`` with ``want_saved``, else None."""
+    for ``gated_ffn_bwd`` with ``want_saved``, else None. They are kept in ``saved_dtype``: fp32
+    (``GDR_FFN_KEEP_F32``), or x's dtype, which for bf16 takes half the memory and leaves gradients a
+    third less exact."""
     dims, dev = _ffn_args(x, w_gate, w_up, act)
+    if want_saved:
+        _keep(dims, saved_dtype, x.dtype, "saved_dtype")
     shape = tuple(x.shape[:-1]) + (dims.F,)
     if out is None:
         out = torch.empty(shape, dtype=x.dtype, device=dev)
     else:
         _need(out, "out", x.dtype, shape, dev)
-    gate = torch.empty_like(out) if want_saved else None
-    up = torch.empty_like(out) if want_saved else None
+    gate = torch.empty(shape, dtype=saved_dtype, device=dev) if want_saved else None
+    up = torch.empty_like(gate) if want_saved else None
     _check(lib().gdr_gated_ffn_fwd(_ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(out), _ptr(gate), _ptr(up),
                                    ctypes.byref(dims), _stream(x)))
     return out, gate, up
 
 
 def gated_ffn_bwd(x, w_gate, w_up, gate, up, dh, *, act: str = "silu", workspace=None):
-    """Gradients of ``gated_ffn_fwd`` (``gdr_gated_ffn_bwd``): its inputs, the gate and up it kept and
-    dh [..., F]. Returns (dx [..., D], dw_gate, dw_up [F, D]) in x's dtype."""
+    """Gradients of ``gated_ffn_fwd`` (``gdr_gated_ffn_bwd``): its inputs, the gate and up it kept (fp32 or
+    x's dtype, both the same) and dh [..., F]. Returns (dx [..., D], dw_gate, dw_up [F, D]) in x's dtype."""
     dims, dev = _ffn_args(x, w_gate, w_up, act)
     shape = tuple(x.shape[:-1]) + (dims.F,)
-    for t, n in ((gate, "gate"), (up, "up"), (dh, "dh")):
-        _need(t, n, x.dtype, shape, dev)
+    _need(gate, "gate", None, shape, dev)
+    _keep(dims, gate.dtype, x.dtype, "gate")
+    _need(up, "up", gate.dtype, shape, dev)
+    _need(dh, "dh", x.dtype, shape, dev)
     dx, dwg, dwu = torch.empty_like(x), torch.empty_like(w_gate), torch.empty_like(w_up)
     ws = _workspace(workspace, lib().gdr_gated_ffn_bwd_workspace_bytes(ctypes.byref(dims)), dev)
     _check(lib().gdr_gated_ffn_bwd(_ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(gate), _ptr(up), _ptr(dh), _ptr(dx),

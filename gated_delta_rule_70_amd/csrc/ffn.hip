@@ -5,11 +5,11 @@
 //   dU = dh * act(G),  dG = dh * U * act'(G)
 //   dx = dG Wg + dU Wu,  dWg = dG^T x,  dWu = dU^T x
 //
-// Products are summed in 32 bits. With bf16 inputs G and U are kept in bf16 for the backward and
-// dG, dU enter its products in bf16: each is one rounding of a matrix operand, of the size of the
-// inputs' own. The gradients are 3.1e-3 (relative Frobenius) off the 64-bit ones that way, where
-// keeping everything in 32 bits up to the results' own rounding gives 1.7e-3; products of two bf16
-// halves a value would double the backward's matrix instructions.
+// Products are summed in 32 bits. With bf16 inputs dG and dU enter the backward's products in bf16: one rounding of a
+// matrix operand, of the size of the inputs' own (products of two bf16 halves a value would double the
+// backward's matrix instructions). G and U are kept for the backward in 32 bits, or in bf16 where the caller would rather
+// have the memory: gradients (relative Frobenius, against 64 bits) 2.3e-3 off and a training pass of 16384 tokens, 2048 x
+// 8192, in 3.36 ms, or 3.1e-3 and 3.12 ms; the results' own rounding alone is 1.7e-3.
 //
 // Matrix instructions bound the large sizes: 16384 tokens, 2048 x 8192, bf16: forward with G and U kept
 // 1148 us (958 TFLOP/s; 0.11 ms less without G and U, whose 537 MB of stores come in bursts at
@@ -45,9 +45,11 @@ __device__ __forceinline__ void act_grad_f(float x, int act, float &val, float &
     der = q + x * q * (1.f - q) * ds;
 }
 
-template <typename E>
+// S: the type gate and up are kept in
+template <typename E, typename S>
 struct GluEpi {
-    E *h, *gate, *up;
+    E *h;
+    S *gate, *up;
     int64_t M, F;
     int act;
     static constexpr bool whole = true;
@@ -62,8 +64,8 @@ struct GluEpi {
                 for (int r = 0; r < 4; ++r) v[j][r] = act_f(acc[0][i][j][r], act) * acc[1][i][j][r];
             store_rows<E, MI, NI>(st, v, h, F, m0 + 16 * i, n0, M, F);
             if (gate) {
-                store_rows<E, MI, NI>(st, acc[0][i], gate, F, m0 + 16 * i, n0, M, F);
-                store_rows<E, MI, NI>(st, acc[1][i], up, F, m0 + 16 * i, n0, M, F);
+                store_rows<S, MI, NI>(st, acc[0][i], gate, F, m0 + 16 * i, n0, M, F);
+                store_rows<S, MI, NI>(st, acc[1][i], up, F, m0 + 16 * i, n0, M, F);
             }
         }
     }
@@ -72,60 +74,61 @@ struct GluEpi {
 // dG and dU, rows of ld elements, columns F .. ld-1 zero; 16 bytes of each a thread. Bound by memory: three
 // reads and two writes, 1.34 GB for 16384 x 8192 bf16 in 256 us (5.2 TB/s; 388 us with 2 bytes a thread).
 // Apart from the products: each value of dG and dU is an operand of two of them.
-template <typename E>
-__global__ __launch_bounds__(256) void glu_grad_kernel(const E *gate, const E *up, const E *dh, E *dg, E *du, int64_t M,
+template <typename E, typename S, typename G>
+__global__ __launch_bounds__(256) void glu_grad_kernel(const S *gate, const S *up, const E *dh, G *dg, G *du, int64_t M,
                                                        int64_t F, int64_t ld, int act) {
     constexpr int V = 16 / sizeof(E);
     typedef E Piece __attribute__((ext_vector_type(V)));
+    typedef S Kept __attribute__((ext_vector_type(V), aligned(16)));
+    typedef G Grad __attribute__((ext_vector_type(V), aligned(16)));
     const int64_t i = block_id() * 256 + threadIdx.x, pieces = ld / V;
     if (i >= M * pieces) return;
     const int64_t m = i / pieces, n = (i - m * pieces) * V, k = m * F + n;
-    Piece g, u, d;
+    Kept g, u;
+    Piece d;
     // Whole pieces inside the row; ld may hold one more than F (fp32, F % 8 == 4), which is all zeros.
     if (F % V == 0 && n < F) {
-        g = *reinterpret_cast<const Piece *>(gate + k);
-        u = *reinterpret_cast<const Piece *>(up + k);
+        g = *reinterpret_cast<const Kept *>(gate + k);
+        u = *reinterpret_cast<const Kept *>(up + k);
         d = *reinterpret_cast<const Piece *>(dh + k);
     } else {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const bool in = n + j < F;
-            g[j] = in ? gate[k + j] : (E)0.f;
-            u[j] = in ? up[k + j] : (E)0.f;
+            g[j] = in ? gate[k + j] : (S)0.f;
+            u[j] = in ? up[k + j] : (S)0.f;
             d[j] = in ? dh[k + j] : (E)0.f;
         }
     }
-    Piece pg, pu;
+    Grad pg, pu;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         float val, der;
         act_grad_f((float)g[j], act, val, der);
         const float dj = (float)d[j];
-        pg[j] = (E)(dj * (float)u[j] * der);
-        pu[j] = (E)(dj * val);
+        pg[j] = (G)(dj * (float)u[j] * der);
+        pu[j] = (G)(dj * val);
     }
-    *reinterpret_cast<Piece *>(dg + i * V) = pg;
-    *reinterpret_cast<Piece *>(du + i * V) = pu;
+    *reinterpret_cast<Grad *>(dg + i * V) = pg;
+    *reinterpret_cast<Grad *>(du + i * V) = pu;
 }
 
-template <typename E>
+template <typename E, typename S>
 hipError_t fwd_t(const FfnArgs &a, hipStream_t s) {
     GemmOp g = ffn_fwd_product(a.M, a.D, a.F);
     g.A[0] = a.x;
     g.B[0] = a.wg, g.B[1] = a.wu;
-    return launch_gemm<E, true, true, 2>(g, GluEpi<E>{(E *)a.h, (E *)a.gate, (E *)a.up, a.M, a.F, a.act}, s);
+    return launch_gemm<E, true, true, 2>(g, GluEpi<E, S>{(E *)a.h, (S *)a.gate, (S *)a.up, a.M, a.F, a.act}, s);
 }
 
 // the products of the backward: dx, and both weights' gradients side by side
-template <typename E>
-GemmOp dx_op(const FfnArgs &a, const E *dg, const E *du) {
+GemmOp dx_op(const FfnArgs &a, const void *dg, const void *du) {
     GemmOp g = ffn_dx_product(a.M, a.D, a.F);
     g.A[0] = dg, g.A[1] = du;
     g.B[0] = a.wg, g.B[1] = a.wu;
     return g;
 }
-template <typename E>
-GemmOp dw_op(const FfnArgs &a, const E *dg, const E *du) {
+GemmOp dw_op(const FfnArgs &a, const void *dg, const void *du) {
     GemmOp g = ffn_dw_product(a.M, a.D, a.F);
     g.A[0] = dg, g.A[1] = du;
     g.B[0] = g.B[1] = a.x;
@@ -134,28 +137,36 @@ GemmOp dw_op(const FfnArgs &a, const E *dg, const E *du) {
 // workspace: dG and dU, then the partial products of one product at a time
 template <typename E>
 int64_t bwd_bytes(const FfnArgs &a) {
-    const E *none = nullptr;
-    const int64_t x = store_ws_bytes<E>(dx_op(a, none, none)), w = store_ws_bytes<E>(dw_op(a, none, none));
-    return 2 * a.M * grad_ld(a.F) * (int64_t)sizeof(E) + (x > w ? x : w);
+    const int64_t x = store_ws_bytes<E>(dx_op(a, nullptr, nullptr)), w = store_ws_bytes<E>(dw_op(a, nullptr, nullptr));
+    const int64_t es = whole_pieces(a.D, sizeof(E)) ? sizeof(E) : 4;
+    return 2 * a.M * grad_ld(a.F) * es + (x > w ? x : w);
 }
 
-template <typename E>
+// G: the type of dG and dU. Where rows of D elements are not whole 16-byte pieces both products run on fp32 matrix
+// instructions, and dG and dU are left in 32 bits.
+template <typename E, typename S, typename G>
 hipError_t bwd_t(const FfnArgs &a, hipStream_t s) {
     const int64_t ld = grad_ld(a.F);
-    E *dg = (E *)a.ws, *du = dg + a.M * ld;
+    G *dg = (G *)a.ws, *du = dg + a.M * ld;
+    const StoreEpi<E> to_x{{(E *)a.dx, nullptr}, nullptr, nullptr, nullptr, nullptr, a.M, a.D, a.D},
+        to_w{{(E *)a.dwg, (E *)a.dwu}, nullptr, nullptr, nullptr, nullptr, a.F, a.D, a.D};
     void *part = du + a.M * ld;
     if (a.M > 0) {
         const int64_t blocks = (a.M * ld / (16 / (int64_t)sizeof(E)) + 255) / 256;
-        hipLaunchKernelGGL((glu_grad_kernel<E>), grid_of(blocks, 256), dim3(256), 0, s, (const E *)a.gate,
-                           (const E *)a.up, (const E *)a.dh, dg, du, a.M, a.F, ld, a.act);
+        hipLaunchKernelGGL((glu_grad_kernel<E, S, G>), grid_of(blocks, 256), dim3(256), 0, s, (const S *)a.gate,
+                           (const S *)a.up, (const E *)a.dh, dg, du, a.M, a.F, ld, a.act);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        e = launch_gemm_store<E, true, false>(
-            dx_op(a, dg, du), StoreEpi<E>{{(E *)a.dx, nullptr}, nullptr, nullptr, nullptr, nullptr, a.M, a.D, a.D}, part, s);
+        if constexpr (sizeof(G) > sizeof(E)) e = launch_gemm_any_op<G, E, true, false, 1>(dx_op(a, dg, du), to_x, s);
+        else e = launch_gemm_store<E, true, false>(dx_op(a, dg, du), to_x, part, s);
         if (e != hipSuccess) return e;
     }
-    return launch_gemm_store<E, false, false>(
-        dw_op(a, dg, du), StoreEpi<E>{{(E *)a.dwg, (E *)a.dwu}, nullptr, nullptr, nullptr, nullptr, a.F, a.D, a.D}, part, s);
+    if constexpr (sizeof(G) > sizeof(E)) return launch_gemm_any_op<G, E, false, false, 1>(dw_op(a, dg, du), to_w, s);
+    else return launch_gemm_store<E, false, false>(dw_op(a, dg, du), to_w, part, s);
+}
+template <typename S>
+hipError_t bwd_bf16(const FfnArgs &a, hipStream_t s) {
+    return whole_pieces(a.D, 2) ? bwd_t<__bf16, S, __bf16>(a, s) : bwd_t<__bf16, S, float>(a, s);
 }
 
 }  // namespace
@@ -169,10 +180,12 @@ int64_t ffn_bwd_ws_bytes(int64_t M, int64_t D, int64_t F, int dtype) {
 }
 
 hipError_t launch_ffn_fwd(const FfnArgs &a, int dtype, hipStream_t s) {
-    return dtype == kDtypeBf16 ? fwd_t<__bf16>(a, s) : fwd_t<float>(a, s);
+    if (dtype != kDtypeBf16) return fwd_t<float, float>(a, s);
+    return a.wide ? fwd_t<__bf16, float>(a, s) : fwd_t<__bf16, __bf16>(a, s);
 }
 hipError_t launch_ffn_bwd(const FfnArgs &a, int dtype, hipStream_t s) {
-    return dtype == kDtypeBf16 ? bwd_t<__bf16>(a, s) : bwd_t<float>(a, s);
+    if (dtype != kDtypeBf16) return bwd_t<float, float, float>(a, s);
+    return a.wide ? bwd_bf16<float>(a, s) : bwd_bf16<__bf16>(a, s);
 }
 
 }  // namespace gdr

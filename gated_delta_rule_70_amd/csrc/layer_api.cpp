@@ -127,7 +127,8 @@ gdr_status_t ffn_sizes(const gdr_ffn_dims_t *dims) {
     const gdr_ffn_dims_t &d = *dims;
     const gdr_status_t s = check_dtype(d.dtype);
     if (s != GDR_OK) return s;
-    if (d.act != GDR_ACT_SILU && d.act != GDR_ACT_GELU_TANH)
+    const int32_t act = d.act & ~GDR_FFN_KEEP_F32;
+    if (act != GDR_ACT_SILU && act != GDR_ACT_GELU_TANH)
         return fail(GDR_ERR_FLAGS, "act %d is not GDR_ACT_SILU or GDR_ACT_GELU_TANH", d.act);
     if (d.M < 0 || d.D < 1 || d.F < 1 || d.D > kMaxWidth || d.F > kMaxWidth || d.M > INT32_MAX)
         return fail(GDR_ERR_DIMS, "M (%lld) must be in [0, 2^31), D (%lld) and F (%lld) in [1, 2^20]", (long long)d.M, (long long)d.D, (long long)d.F);
@@ -136,6 +137,10 @@ gdr_status_t ffn_sizes(const gdr_ffn_dims_t *dims) {
         return fail(GDR_ERR_DIMS, "M (%lld) is too large for these widths", (long long)d.M);
     return GDR_OK;
 }
+
+// the type gate and up are kept in: dtype, or fp32
+bool ffn_wide(const gdr_ffn_dims_t &d) { return (d.act & GDR_FFN_KEEP_F32) != 0; }
+int64_t ffn_kept_bytes(const gdr_ffn_dims_t &d) { return d.M * d.F * (ffn_wide(d) ? 4 : elem_size(d.dtype)); }
 
 gdr_status_t ce_sizes(const gdr_ce_dims_t *dims) {
     if (!dims) return fail(GDR_ERR_NULL, "dims is NULL");
@@ -268,13 +273,14 @@ gdr_status_t gdr_gated_ffn_fwd(const void *x, const void *w_gate, const void *w_
     const int64_t es = elem_size(d.dtype), nx = d.M * d.D * es, nw = d.F * d.D * es, nh = d.M * d.F * es;
     if (nh > 0 && (gate == nullptr) != (up == nullptr)) return fail(GDR_ERR_NULL, "gate and up are kept together or not at all");
     const Buf ins[] = {Buf("x", x, nx), Buf("w_gate", w_gate, nw), Buf("w_up", w_up, nw)};
-    const Buf outs[] = {Buf("h", h, nh), Buf("gate", gate, nh, true), Buf("up", up, nh, true)};
+    const int64_t nk = ffn_kept_bytes(d);
+    const Buf outs[] = {Buf("h", h, nh), Buf("gate", gate, nk, true), Buf("up", up, nk, true)};
     s = check_buffers(ins, outs);
     if (s != GDR_OK) return s;
     gdr::FfnArgs a{};
     a.x = x; a.wg = w_gate; a.wu = w_up;
     a.h = h; a.gate = gate; a.up = up;
-    a.M = d.M; a.D = d.D; a.F = d.F; a.act = d.act;
+    a.M = d.M; a.D = d.D; a.F = d.F; a.act = d.act & ~GDR_FFN_KEEP_F32; a.wide = ffn_wide(d);
     return launched(gdr::launch_ffn_fwd(a, d.dtype, reinterpret_cast<hipStream_t>(stream)), "gated feed-forward");
 }
 
@@ -291,11 +297,11 @@ gdr_status_t gdr_gated_ffn_bwd(const void *x, const void *w_gate, const void *w_
     if (s != GDR_OK) return s;
     const gdr_ffn_dims_t &d = *dims;
     const int64_t es = elem_size(d.dtype), nx = d.M * d.D * es, nw = d.F * d.D * es, nh = d.M * d.F * es;
-    const int64_t need = gdr::ffn_bwd_ws_bytes(d.M, d.D, d.F, d.dtype);
+    const int64_t need = gdr::ffn_bwd_ws_bytes(d.M, d.D, d.F, d.dtype), nk = ffn_kept_bytes(d);
     s = check_workspace(workspace, workspace_bytes, need);
     if (s != GDR_OK) return s;
     const Buf ins[] = {Buf("x", x, nx), Buf("w_gate", w_gate, nw), Buf("w_up", w_up, nw),
-                       Buf("gate", gate, nh), Buf("up", up, nh), Buf("dh", dh, nh)};
+                       Buf("gate", gate, nk), Buf("up", up, nk), Buf("dh", dh, nh)};
     const Buf outs[] = {Buf("dx", dx, nx), Buf("dw_gate", dw_gate, nw), Buf("dw_up", dw_up, nw),
                         Buf("workspace", workspace, need, true)};
     s = check_buffers(ins, outs);
@@ -304,7 +310,7 @@ gdr_status_t gdr_gated_ffn_bwd(const void *x, const void *w_gate, const void *w_
     a.x = x; a.wg = w_gate; a.wu = w_up;
     a.gate = const_cast<void *>(gate); a.up = const_cast<void *>(up);
     a.dh = dh; a.dx = dx; a.dwg = dw_gate; a.dwu = dw_up; a.ws = workspace;
-    a.M = d.M; a.D = d.D; a.F = d.F; a.act = d.act;
+    a.M = d.M; a.D = d.D; a.F = d.F; a.act = d.act & ~GDR_FFN_KEEP_F32; a.wide = ffn_wide(d);
     return launched(gdr::launch_ffn_bwd(a, d.dtype, reinterpret_cast<hipStream_t>(stream)), "gated feed-forward backward");
 }
 

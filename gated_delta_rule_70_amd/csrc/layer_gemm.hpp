@@ -36,7 +36,8 @@ struct AnyGemmArgs {
 // loads and LDS accesses are of single elements, which bounds it: 1021 x 2 x 2731 x 1023 fp32 takes 265 us (43 TFLOP/s), against 127 us in
 // gemm_tile_kernel for a width of 1024.
 constexpr int kAnyK = 16, kAnyLd = kAnyK + 1, kSumK = 512;
-template <typename E, int NB, class Epi>
+// EA and EB: the operands' types.
+template <typename EA, typename EB, int NB, class Epi>
 __global__ __launch_bounds__(256) void gemm_any_kernel(AnyGemmArgs a, Epi epi) {
     __shared__ float As[64 * kAnyLd], Bs[NB][64 * kAnyLd];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
@@ -54,7 +55,7 @@ __global__ __launch_bounds__(256) void gemm_any_kernel(AnyGemmArgs a, Epi epi) {
     };
     each([](floatx4 &p, floatx4 &t) { p = t = zero4(); });
 
-    auto stage = [&](float *dst, const E *src, int64_t r0, int64_t rows, int64_t k0, int64_t sr, int64_t sk) {
+    auto stage = [&](float *dst, const auto *src, int64_t r0, int64_t rows, int64_t k0, int64_t sr, int64_t sk) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int row = sk == 1 ? tid / 16 + 16 * j : tid % 64, k = sk == 1 ? tid % 16 : tid / 64 + 4 * j;
@@ -65,9 +66,9 @@ __global__ __launch_bounds__(256) void gemm_any_kernel(AnyGemmArgs a, Epi epi) {
     };
     for (int p = 0; p < a.pairs; ++p)
         for (int64_t k0 = 0; k0 < a.K; k0 += kAnyK) {
-            stage(As, (const E *)a.A[p], m0, a.M, k0, a.am, a.ak);
+            stage(As, (const EA *)a.A[p], m0, a.M, k0, a.am, a.ak);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) stage(Bs[b], (const E *)a.B[NB == 2 ? b : p], n0, a.N, k0, a.bn, a.bk);
+            for (int b = 0; b < NB; ++b) stage(Bs[b], (const EB *)a.B[NB == 2 ? b : p], n0, a.N, k0, a.bn, a.bk);
             __syncthreads();
 #pragma unroll
             for (int k = 0; k < kAnyK; k += 4)
@@ -87,12 +88,12 @@ __global__ __launch_bounds__(256) void gemm_any_kernel(AnyGemmArgs a, Epi epi) {
     epi(acc, m0 + wm, n0 + wn, a.batch, nullptr);
 }
 
-template <typename E, int NB, class Epi>
+template <typename EA, typename EB, int NB, class Epi>
 hipError_t launch_gemm_any(const AnyGemmArgs &a, const Epi &epi, hipStream_t s) {
     const int64_t blocks = ((a.M + 63) / 64) * ((a.N + 63) / 64);
     if (blocks == 0) return hipSuccess;
     if (blocks > INT32_MAX) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((gemm_any_kernel<E, NB, Epi>), grid_of(blocks, 256), dim3(256), 0, s, a, epi);
+    hipLaunchKernelGGL((gemm_any_kernel<EA, EB, NB, Epi>), grid_of(blocks, 256), dim3(256), 0, s, a, epi);
     return hipGetLastError();
 }
 
@@ -636,6 +637,18 @@ hipError_t launch_gemm_rows(const TileGemmArgs &a, const Epi &epi, hipStream_t s
     return hipGetLastError();
 }
 
+// The product on gemm_any_kernel, the products side by side one after the other.
+template <typename EA, typename EB, bool AKC, bool BKC, int NB, class Epi>
+hipError_t launch_gemm_any_op(const GemmOp &o, const Epi &epi, hipStream_t s) {
+    for (int b = 0; b < o.batch; ++b) {
+        const AnyGemmArgs g{{o.A[b], o.A[1]}, {o.B[b], o.B[1]}, AKC ? o.lda : 1, AKC ? 1 : o.lda, BKC ? o.ldb : 1,
+                            BKC ? 1 : o.ldb, o.M, o.N, o.K, o.pairs, b};
+        const hipError_t e = launch_gemm_any<EA, EB, NB>(g, epi, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 // The product in the order given by AKC and BKC (true: k contiguous, the leading dimension between rows; false:
 // rows contiguous, the leading dimension between k), on the kernel that path_of names.
 template <typename E, bool AKC, bool BKC, int NB, class Epi>
@@ -659,13 +672,7 @@ hipError_t launch_gemm(const GemmOp &o, const Epi &epi, hipStream_t s) {
         if (how.tile == 128) return launch_gemm_tile<E, AKC, BKC, NB, 128, 128, 4, 2, 2>(t, epi, s);
         return launch_gemm_tile<E, AKC, BKC, NB, 64, 128, 2, 2, 3>(t, epi, s);
     }
-    for (int b = 0; b < o.batch; ++b) {
-        const AnyGemmArgs g{{o.A[b], o.A[1]}, {o.B[b], o.B[1]}, AKC ? o.lda : 1, AKC ? 1 : o.lda, BKC ? o.ldb : 1,
-                            BKC ? 1 : o.ldb, o.M, o.N, o.K, o.pairs, b};
-        const hipError_t e = launch_gemm_any<E, NB>(g, epi, s);
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+    return launch_gemm_any_op<E, E, AKC, BKC, NB>(o, epi, s);
 }
 
 // ---------------------------------------------------------------- stores

@@ -37,13 +37,14 @@ struct ScanArgs {
 
 struct FfnArgs {
     const void *x, *wg, *wu;        // [M][D], [F][D], [F][D]
-    void *h, *gate, *up;            // [M][F]; gate, up null unless kept
+    void *h, *gate, *up;            // [M][F]; gate, up null unless kept, in fp32 with `wide`
     // backward (gate and up as the forward kept them)
     const void *dh;
     void *dx, *dwg, *dwu;
     void *ws;
     int64_t M, D, F;
     int act;
+    bool wide;
 };
 
 struct CeArgs {

@@ -517,27 +517,31 @@ gdr_status_t gdr_channel_scan_step(const void *x, const void *a, const void *b, 
  */
 typedef enum gdr_act { GDR_ACT_SILU = 0, GDR_ACT_GELU_TANH = 1 } gdr_act_t;
 
+#define GDR_FFN_KEEP_F32 256 /* or'ed into act: gate and up are kept in fp32 */
+
 typedef struct gdr_ffn_dims {
     int64_t M;     /* tokens, >= 0 */
     int64_t D;     /* input width, 1 .. 2^20 */
     int64_t F;     /* hidden width, 1 .. 2^20 */
     int32_t dtype; /* gdr_dtype_t of every tensor */
-    int32_t act;   /* gdr_act_t */
+    int32_t act;   /* gdr_act_t, GDR_FFN_KEEP_F32 */
 } gdr_ffn_dims_t;
 
 /*
  * gdr_gated_ffn_fwd - both projections, the activation and the product in one kernel.
  *
  *   x [M][D];  w_gate, w_up [F][D];  h [M][F]
- *   gate, up [M][F]: G and U, kept (in dtype) for the backward; both NULL when not wanted
+ *   gate, up [M][F]: G and U, kept for the backward in dtype, or in fp32 with GDR_FFN_KEEP_F32; both
+ *            NULL when not wanted
  *
  * gdr_gated_ffn_bwd - gradients of sum(h * dh): dx [M][D], dw_gate and dw_up [F][D], from x, the
- * weights, gate and up as the forward kept them and dh [M][F]; every tensor in dtype. workspace: at
+ * weights, gate and up as the forward kept them (act as given to it) and dh [M][F]; every other tensor
+ * in dtype. workspace: at
  * least gdr_gated_ffn_bwd_workspace_bytes(dims) bytes.
  *
- * Products are summed in fp32. With bf16 inputs G and U are rounded to bf16 where they are kept
- * (h itself is formed from the unrounded ones), and dG and dU where they enter the backward's
- * products. Rows of any width are taken; D a multiple of 16 bytes is the fast case.
+ * Products are summed in fp32. With bf16 inputs dG and dU are rounded to bf16 where they enter the
+ * backward's products, and G and U where they are kept without GDR_FFN_KEEP_F32 (h itself is formed
+ * from the unrounded ones): half the memory, and gradients that are a third less exact. Rows of any width are taken; D a multiple of 16 bytes is the fast case.
  * Errors as gdr_channel_scan_fwd; GDR_ERR_FLAGS for an unknown act.
  */
 gdr_status_t gdr_gated_ffn_fwd(const void *x, const void *w_gate, const void *w_up, void *h,

@@ -207,3 +207,65 @@ def test_slope_of_huge_gates(gdr, act, dtype):
     assert not dx.any()
     for got, ref in ((dwg, slope), (dwu, val)):
         assert (abs(L.f64(got) - ref[:, None]) <= BWD[dtype] * (1.0 + abs(ref[:, None]))).all()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("M,D,F", [(300, 256, 320), (33, 512, 1000), (1000, 520, 1301), (2050, 1032, 2200), (300, 100, 333)])
+def test_gradients_with_two_roundings(gdr, M, D, F, act):
+    """bf16 with gate and up kept in fp32, as is the default: dG and dU are rounded as operands and the gradients as
+    results, each about 1.65e-3 of them at random, 2.35e-3 together; a third rounding makes it 2.9e-3 and more."""
+    say("gated ffn M %d D %d F %d %s" % (M, D, F, act))
+    x, wg, wu, dh = make(M, D, F, BF16, 20)
+    gx, gwg, gwu, gdh = (t.cuda() for t in (x, wg, wu, dh))
+    h, gate, up = gdr.gated_ffn_fwd(gx, gwg, gwu, act=act, want_saved=True)
+    assert gate.dtype == up.dtype == FP32
+    check(gate, L.f64(x) @ L.f64(wg).T, FWD[FP32], "gate")
+    check(up, L.f64(x) @ L.f64(wu).T, FWD[FP32], "up")
+    got = gdr.gated_ffn_bwd(gx, gwg, gwu, gate, up, gdh, act=act)
+    for name, p, q in zip(("dx", "dw_gate", "dw_up"), got, L.ffn_grads(x, wg, wu, dh, act)):
+        assert p.dtype == BF16
+        check(p, q, 2.6e-3, name)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("M,D,F", [(1, 64, 96), (40, 64, 97), (300, 256, 320), (2049, 264, 515), (5558, 1864, 2199), (30, 33, 50)])
+def test_kept_in_bf16(gdr, M, D, F, act):
+    say("gated ffn, kept in bf16, M %d D %d F %d %s" % (M, D, F, act))
+    x, wg, wu, dh = make(M, D, F, BF16, 21)
+    gx, gwg, gwu, gdh = (t.cuda() for t in (x, wg, wu, dh))
+    h, gate, up = gdr.gated_ffn_fwd(gx, gwg, gwu, act=act, want_saved=True, saved_dtype=BF16)
+    h2, gate2, up2 = gdr.gated_ffn_fwd(gx, gwg, gwu, act=act, want_saved=True)
+    assert torch.equal(h, h2) and torch.equal(gate, gate2.bfloat16()) and torch.equal(up, up2.bfloat16())
+    got = gdr.gated_ffn_bwd(gx, gwg, gwu, gate, up, gdh, act=act)
+    wide = gdr.gated_ffn_bwd(gx, gwg, gwu, gate.float(), up.float(), gdh, act=act)
+    assert all(torch.equal(p, q) for p, q in zip(got, wide))
+    for name, p, q in zip(("dx", "dw_gate", "dw_up"), got, L.ffn_grads(x, wg, wu, dh, act)):
+        check(p, q, BWD[BF16], name)
+
+
+def test_refusals_of_kept_types(gdr):
+    x, wg, wu, dh = (t.cuda() for t in make(6, 16, 24, BF16, 22))
+    h, gate, up = gdr.gated_ffn_fwd(x, wg, wu, want_saved=True)
+    with pytest.raises(ValueError, match="saved_dtype must be"):
+        gdr.gated_ffn_fwd(x, wg, wu, want_saved=True, saved_dtype=torch.float16)
+    with pytest.raises(ValueError, match="saved_dtype must be"):
+        gdr.gated_ffn_fwd(x.float(), wg.float(), wu.float(), want_saved=True, saved_dtype=BF16)
+    with pytest.raises(ValueError, match="up must be"):
+        gdr.gated_ffn_bwd(x, wg, wu, gate, up.bfloat16(), dh)
+    with pytest.raises(ValueError, match="gate must be"):
+        gdr.gated_ffn_bwd(x, wg, wu, gate.half(), up.half(), dh)
+    with pytest.raises(ValueError, match="dh must be"):
+        gdr.gated_ffn_bwd(x, wg, wu, gate, up, dh.float())
+
+
+@pytest.mark.parametrize("M,D,F", [(300, 33, 50), (300, 100, 333), (40, 513, 64), (1021, 12, 801)])
+def test_gradients_with_one_rounding(gdr, M, D, F):
+    """bf16 rows that are not whole 16-byte pieces: the products are fp32 ones, dG and dU enter them unrounded, and only
+    the results are rounded, 1.65e-3 of them at random (some thousand values at least: within 0.25e-3 of that)."""
+    say("gated ffn M %d D %d F %d" % (M, D, F))
+    x, wg, wu, dh = make(M, D, F, BF16, 23)
+    gx, gwg, gwu, gdh = (t.cuda() for t in (x, wg, wu, dh))
+    h, gate, up = gdr.gated_ffn_fwd(gx, gwg, gwu, want_saved=True)
+    got = gdr.gated_ffn_bwd(gx, gwg, gwu, gate, up, gdh)
+    for name, p, q in zip(("dx", "dw_gate", "dw_up"), got, L.ffn_grads(x, wg, wu, dh)):
+        check(p, q, 1.9e-3, name)

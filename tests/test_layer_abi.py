@@ -134,3 +134,15 @@ def test_sizes_of_an_empty_batch(T, dtype):
     d = binding.ScanDims(0, T, 20, 0, dtype, 0)
     for f in (lib.gdr_channel_scan_states_elems, lib.gdr_channel_scan_fwd_workspace_bytes, lib.gdr_channel_scan_bwd_workspace_bytes):
         assert f(ctypes.byref(d), 0) == 0
+
+
+def test_type_of_the_kept_projections():
+    """With gate and up in fp32 each is twice as long as bf16 ones, and the activation is still checked."""
+    at = A * 5 + 8 * 24 * 2
+    got, msg = call("ffn_fwd", dict(act=256, up=at))
+    assert got == "GDR_ERR_ALIAS" and "gate overlaps up" in msg
+    got, msg = call("ffn_bwd", dict(act=256, dx=A * 4 + 8 * 24 * 2))
+    assert got == "GDR_ERR_ALIAS" and "dx overlaps gate" in msg
+    for act in (257 + 1, 512, -1):
+        got, msg = call("ffn_fwd", dict(act=act))
+        assert got == "GDR_ERR_FLAGS" and "act" in msg
