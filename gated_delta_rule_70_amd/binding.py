@@ -784,8 +784,8 @@ def gated_ffn_fwd(x, w_gate, w_up, *, act: str = "silu", out=None, want_saved: b
     (``gdr_gated_ffn_fwd``): h = act(x w_gate^T) * (x w_up^T). x [..., D]; w_gate, w_up [F, D] (bf16
     or fp32, one dtype). Returns (h [..., F], gate, up); the projections gate and up [..., F] are kept
     for ``gated_ffn_bwd`` with ``want_saved``, else None. They are kept in ``saved_dtype``: fp32
-    (``GDR_FFN_KEEP_F32``), or x's dtype, which for bf16 takes half the memory and leaves gradients a
-    third less exact."""
+    (``GDR_FFN_KEEP_F32``), or x's dtype, which for bf16 takes half the memory and leaves a third more
+    error in the gradients."""
     dims, dev = _ffn_args(x, w_gate, w_up, act)
     if want_saved:
         _keep(dims, saved_dtype, x.dtype, "saved_dtype")

@@ -26,12 +26,17 @@
 // chunks before its own (behind it, in the backward) before it starts, at the cost of reading the
 // inputs of the maps twice.
 //
-// Measured (bf16): 4 x 4096 tokens x 2048 channels forward 72 us (268 MB, 3.7 TB/s), backward 127 us
-// (470 MB, 3.7 TB/s); the device's own large copy moves 4.9 TB/s. Per element the gates are 5
+// Measured (bf16): 4 x 4096 tokens x 2048 channels forward 71 us (268 MB, 3.8 TB/s), backward 133 us
+// (470 MB, 3.5 TB/s); the device's own large copy moves 4.9 TB/s. Per element the gates are 5
 // transcendental and about 25 other instructions, which at eight waves a compute unit nearly take the
-// time that the bytes take and do not all hide behind them. Split, 131,072 tokens x 1024 channels:
-// 219 us for the maps (805 MB, 3.7 TB/s) and 267 us for the scan (1074 MB, 4.0 TB/s). The chunks'
+// time that the bytes take and do not all hide behind them. The backward holds 245 registers (fp32: 160), so that
+// a compute unit has one workgroup of it. Split, 131,072 tokens x 1024 channels:
+// 217 us for the maps (805 MB, 3.7 TB/s) and 265 us for the scan (1074 MB, 4.0 TB/s). The chunks'
 // order is fixed, so the results do not depend on which workgroup comes first.
+//
+// A sequence takes whole blocks, so short ones leave slots idle: 2^14 tokens x 2048 channels as sequences of 4096, 256,
+// 64, 16 and 1 tokens take 60, 53, 184, 680 and 10310 us forward and 133, 151, 506, 1920 and 29,280 us backward. (One
+// token at a time without a gradient is scan_step_kernel's.)
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>

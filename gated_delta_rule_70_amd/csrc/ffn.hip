@@ -11,10 +11,10 @@
 // have the memory: gradients (relative Frobenius, against 64 bits) 2.3e-3 off and a training pass of 16384 tokens, 2048 x
 // 8192, in 3.36 ms, or 3.1e-3 and 3.12 ms; the results' own rounding alone is 1.7e-3.
 //
-// Matrix instructions bound the large sizes: 16384 tokens, 2048 x 8192, bf16: forward with G and U kept
-// 1148 us (958 TFLOP/s; 0.11 ms less without G and U, whose 537 MB of stores come in bursts at
-// each tile's end), dx 915 us (1202 TFLOP/s), both weights' gradients 913 us (1205). The weights' read
-// bounds few tokens: one token 14.8 us (67 MB, 4.5 TB/s), 256 tokens 24.3 us.
+// Matrix instructions bound the large sizes: 16384 tokens, 2048 x 8192, bf16: forward 932 us (1180 TFLOP/s), 1048 with G
+// and U kept in bf16 and 1190 in fp32 (their 537 MB and 1074 MB of stores come in bursts at each tile's end), dx
+// 839 us (1311 TFLOP/s), both weights' gradients 818 us (1344). The weights' read
+// bounds few tokens: one token 14.8 us (67 MB, 4.5 TB/s), 256 tokens 24.8 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -71,8 +71,9 @@ struct GluEpi {
     }
 };
 
-// dG and dU, rows of ld elements, columns F .. ld-1 zero; 16 bytes of each a thread. Bound by memory: three
-// reads and two writes, 1.34 GB for 16384 x 8192 bf16 in 256 us (5.2 TB/s; 388 us with 2 bytes a thread).
+// dG and dU, rows of ld elements, columns F .. ld-1 zero; 16 bytes of dh a thread. Bound by memory: three
+// reads and two writes, for 16384 x 8192 bf16 1.34 GB in 256 us (5.2 TB/s; 388 us with 2 bytes a thread), with gate and
+// up in fp32 1.88 GB in 367 us (5.1 TB/s).
 // Apart from the products: each value of dG and dU is an operand of two of them.
 template <typename E, typename S, typename G>
 __global__ __launch_bounds__(256) void glu_grad_kernel(const S *gate, const S *up, const E *dh, G *dg, G *du, int64_t M,

@@ -33,8 +33,8 @@ struct AnyGemmArgs {
 // instructions, every load checked. Four waves of 32 x 32. The sum over k is taken in blocks of
 // kSumK terms that are added up afterwards: one running fp32 sum over the 60,000 tokens of a weight
 // gradient was 2.1e-5 off (relative Frobenius), in blocks the error stops growing with the length. Its
-// loads and LDS accesses are of single elements, which bounds it: 1021 x 2 x 2731 x 1023 fp32 takes 265 us (43 TFLOP/s), against 127 us in
-// gemm_tile_kernel for a width of 1024.
+// loads and LDS accesses are of single elements, which bounds it: 1021 x 2 x 2731 x 1023 takes 257 us in fp32 and 250 in bf16 (44 and 46 TFLOP/s), against 125 and 43 us
+// in gemm_tile_kernel for a width of 1024; with an operand whose k is strided 17 TFLOP/s.
 constexpr int kAnyK = 16, kAnyLd = kAnyK + 1, kSumK = 512;
 // EA and EB: the operands' types.
 template <typename EA, typename EB, int NB, class Epi>
@@ -127,7 +127,7 @@ hipError_t launch_gemm_any(const AnyGemmArgs &a, const Epi &epi, hipStream_t s) 
 // runs at a time are neighbours (its L2 holds their operand rows): workgroup i runs on XCD i % 8 and
 // takes tiles from the i % 8 th contiguous eighth, in columns of eight tiles of m.
 //
-// Bound by the matrix instructions and their feeding: 1.2 to 1.28 PFLOP/s on the large bf16 products
+// Bound by the matrix instructions and their feeding: 1.2 to 1.34 PFLOP/s on the large bf16 products
 // (16384 x 16384 x 2048 and the like; the instruction alone, operands in registers, sustains 2.05; the
 // large tile holds one wave a SIMD, so what a wave waits for at a hand-over is not hidden), 92 TFLOP/s
 // on 1021 x 2731 x 1024 fp32, whose tiles do not fill the last round.
@@ -316,7 +316,9 @@ __global__ __launch_bounds__(64 * WM * WN, (BM / WM) * (BN / WN) > 128 * 64 ? 1 
     const int wm = wave % WM, wn = wave / WM;
 
     // The arguments are read where they are used, once a tile: held through the loop they do not fit
-    // the scalar registers (45 to 70 of them were spilled to vector registers and back in every block).
+    // the scalar registers (45 to 70 of them were spilled to vector registers and back in every block; what is
+    // spilled now, 70 where the large tile reduces logits, 44 where it forms dl and 12 elsewhere, is nearly all
+    // outside the loop over k).
     typedef __attribute__((address_space(4))) const char arg_char;
     auto arg_at = [](int at) GDR_INLINE {
         arg_char *p = (arg_char *)__builtin_amdgcn_kernarg_segment_ptr() + at;
@@ -559,7 +561,7 @@ hipError_t launch_gemm_tile(TileGemmArgs a, const Epi &epi, hipStream_t s) {
 // rows come from L2 (rows past M repeat the last one; their columns are not stored). Both operands k
 // contiguous, rows whole 16-byte pieces. Bound by that read: feed-forward forward of one token, 2048 x 8192
 // (67 MB of weights), 14.8 us (4.5 TB/s), 23.3 us with the tiled kernel; 16 tokens in 65,536 columns
-// of 2048 (268 MB) 67 us (4.0 TB/s).
+// of 2048 (268 MB) 68 us (3.9 TB/s).
 template <typename E, int NB, int MT, int NT, class Epi>
 __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void gemm_rows_kernel(TileGemmArgs a, Epi epi) {
     constexpr int KS = 8 / NT, es = sizeof(E), step = 64 / es, G = 4 / MT;  // step: k of one matrix step; G: turns in flight
