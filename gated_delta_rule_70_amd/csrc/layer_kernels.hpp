@@ -70,7 +70,6 @@ struct AttnRole {
     int32_t da, db;
     bool xk, yk, zk, ok, reverse, in_turned, out_turned, in_slots;  // *_turned: the state is stored as [db][da]
     bool shares;         // mixed form: out is fp32
-    bool fine;           // sequences end with states that go out: formed with three parts to an operand
 };
 
 struct AttnArgs {

@@ -14,9 +14,10 @@
 //   dlog_alpha_t = sum_{s >= t} (q_s . dq_s - k_s . dk_s) + <the adjoint that enters from behind, H there>,
 // with the sum taken to the end of t's segment.
 //
-// Rounding. q, k, v and dout are matrix operands as they are. What is formed from them and is an operand in turn enters as a sum of
-// bf16 numbers. Where a state goes out (in fp32) or the decays' gradient comes of the results (its terms cancel), as three, off by
-// 2^-24 of itself at most; where it only makes results that are rounded to bf16, as two, 2^-16.
+// Rounding. q, k, v and dout are matrix operands as they are. What is formed from them and is an operand in turn (the state, the
+// scores, the decayed rows) enters as a sum of three bf16 numbers, which is off by 2^-25 of it at most: results whose terms cancel
+// are those of fp32 products. Two numbers (2^-17) in the forward and dv took 434 us for 131,072 tokens of 8 heads where three take 474, and 482
+// for 501 in training 4 x 4096 tokens of 16 heads.
 //
 // What bounds it. A chunk of 64 tokens of a 128 x 128 head is 48 KB in, 16 KB out and 6.3 MFLOP (10.5 as executed, in parts). A
 // workgroup of four waves takes 14,600 cycles a chunk with a second one beside it on the compute unit, 12,000 alone (scores 3000,
@@ -160,7 +161,6 @@ __device__ __forceinline__ void write_piece(const Piece<E, N> &p, Rows r, int of
         for (int i = 0; i < (int)sizeof(p) / 16; ++i) __builtin_amdgcn_raw_buffer_store_b128(u.u[i], r, off + 16 * i, 0, kPast);
     }
 }
-__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }  // what follows is not begun earlier
 
 // whether a 16-byte piece holds infinity or NaN (every exponent bit set)
 template <typename E>
@@ -289,7 +289,7 @@ struct Shape {
     static constexpr int NB = 16 * NT * NW;                     // columns of a workgroup
     static constexpr int kPad = 16 / sizeof(E);
     static constexpr int LA = DA + kPad, LB = NB + kPad, LP = C + 4;
-    static constexpr int kPlanes = parts_of<E>(kDots ? 3 : 2);  // parts of the state and the scores as operands
+    static constexpr int kPlanes = parts_of<E>(3);              // parts of the state and the scores as operands
     struct Lds {
         E y[C * LA];
         E z[C * LB];
@@ -431,8 +431,7 @@ __global__ __launch_bounds__(NW * 64, DA > 128 ? 1 : NW / 2) void sweep_kernel(A
         static_assert(C * LP % kElems == 0, "planes are whole pieces");
         for (int i = tid; i < N * C * LP / kElems; i += kThreads) *reinterpret_cast<uintx4 *>(&m.p[i * kElems]) = uintx4{0, 0, 0, 0};
     }
-    const bool outer_end = OUT && (reverse ? sp.first() : sp.last()), ends = outer_end && r.s_out;  // the sequence ends here, and its state is wanted
-    const bool fine = outer_end && r.fine;  // (whether it is wanted or not, so that the results' bits do not depend on that)
+    const bool ends = OUT && r.s_out && (reverse ? sp.first() : sp.last());  // the sequence ends here, and its state is wanted
     double decay = 0.;  // the segment's total, of the states form
     if (nch > 0) {
         if (wave == 0) make_gates<C>(&m.gates[0], la, count(0), reverse);
@@ -652,38 +651,24 @@ __global__ __launch_bounds__(NW * 64, DA > 128 ? 1 : NW / 2) void sweep_kernel(A
             for (int ks = 0; ks < KS; ++ks) {
                 const floatx4 lo = *reinterpret_cast<const floatx4 *>(&gt.on[32 * ks + 4 * g]);
                 const floatx4 hi = *reinterpret_cast<const floatx4 *>(&gt.on[32 * ks + 16 + 4 * g]);
-                // z decayed to the chunk's end, its parts from the first-th on
-                auto decayed = [&](auto first_tag, auto parts_tag) {
-                    constexpr int kFirst = decltype(first_tag)::value, M = decltype(parts_tag)::value;
-                    Parts<E, M - kFirst> zs[NT];
+                Parts<E, N> zs[NT];  // z decayed to the chunk's end
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        floatx4 zl, zh;
+                for (int nt = 0; nt < NT; ++nt) {
+                    floatx4 zl, zh;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            zl[e] = (float)z[ks][nt].lo[e] * lo[e];
-                            zh[e] = (float)z[ks][nt].hi[e] * hi[e];
-                        }
-                        const Parts<E, M> all = parts<E, M>(zl, zh);
-#pragma unroll
-                        for (int q = kFirst; q < M; ++q) zs[nt].part[q - kFirst] = all.part[q];
+                    for (int e = 0; e < 4; ++e) {
+                        zl[e] = (float)z[ks][nt].lo[e] * lo[e];
+                        zh[e] = (float)z[ks][nt].hi[e] * hi[e];
                     }
+                    zs[nt] = parts<E, N>(zl, zh);
+                }
 #pragma unroll
-                    for (int t = 0; t < TA; ++t) {
-                        const Frag<E> y = down<E>(m.y, LA, 16 * t, 4, 32 * ks);
+                for (int t = 0; t < TA; ++t) {
+                    const Frag<E> y = down<E>(m.y, LA, 16 * t, 4, 32 * ks);
 #pragma unroll
-                        for (int q = M - kFirst - 1; q >= 0; --q)
+                    for (int q = N - 1; q >= 0; --q)
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) h[t][nt] = mma32(h[t][nt], y, zs[nt].part[q]);
-                    }
-                };
-                typedef std::integral_constant<int, 0> None;
-                if constexpr (F != kResults || !is_bf16<E>()) {
-                    decayed(None{}, std::integral_constant<int, parts_of<E>(3)>{});
-                } else {
-                    if (__builtin_expect(fine, 0)) decayed(std::integral_constant<int, 2>{}, std::integral_constant<int, 3>{});
-                    in_order();
-                    decayed(None{}, std::integral_constant<int, 2>{});
+                        for (int nt = 0; nt < NT; ++nt) h[t][nt] = mma32(h[t][nt], y, zs[nt].part[q]);
                 }
             }
         }
@@ -997,7 +982,6 @@ hipError_t fwd(const AttnCall &c, hipStream_t s) {
     }
     r.out = c.out;
     r.s_out = c.hT;
-    r.fine = true;
     return sweep<E, kResults>(a, 0, 1, s);
 }
 
@@ -1057,7 +1041,6 @@ hipError_t bwd(const AttnCall &c, hipStream_t s) {
     v.in_slots = k.in_slots;
     v.s_in = k.s_in;
     v.s_out = p.seg ? nullptr : c.dh0;
-    v.fine = !p.seg;
     if (attn_together(dk, dv, p.slots * c.Hv, is_bf16<E>())) {
         v.other = c.dout;  // read and multiplied with as the other roles' are; the products go nowhere
         q.shares = k.shares = group > 1;

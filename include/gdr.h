@@ -612,7 +612,7 @@ gdr_status_t gdr_linear_ce_bwd(const void *x, const void *w, const int64_t *targ
  * all that came before.
  *
  * Every sum is held in fp32 or more, and what is formed from the inputs on the way enters the matrix
- * products with 16 bits or more: of bf16 tensors only out and the gradients of q, k and v are rounded to
+ * products with 24 bits: of bf16 tensors only out and the gradients of q, k and v are rounded to
  * bf16, once. NaN and infinities of a token reach no earlier one. Tokens before cu_seqlens[0] and behind
  * cu_seqlens[num_seqs] belong to no sequence: they are not read, and their rows of the results are not written.
  * Calls that share a workspace must not overlap.
