@@ -266,7 +266,7 @@ __device__ __forceinline__ void make_gates(Gates<C> *t, float la, int n, bool re
     const int lane = threadIdx.x & 63;
     const double own = lane < n ? (double)(la < kLeast ? kLeast : la) * kLog2e : 0.;
     const double v = lane_sums(own), total = from_lane(v, C - 1);
-    const double c = reverse ? v - own : v;
+    const double c = reverse ? moved<0x138, 0xf>(v) : v;  // (backwards up to the token before, whatever this one's decay is)
     if (lane < C) {
         t->c[lane] = c;
         t->in[lane] = ex2((float)c);

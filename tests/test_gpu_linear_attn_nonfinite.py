@@ -1,0 +1,86 @@
+"""Which gradients of linear attention a token that is not finite reaches: those whose formula holds it, and no other.
+
+    dq_t = H_t dout_t    dk_t = G_t v_t    dv_t = G_t^T k_t    dlog_alpha_t = alpha_t <G_t, H_{t-1}>    dh0 = alpha_1 G_1
+
+with H_t of k, v and log_alpha up to t and of h0, and G_t of q and dout from t on, of log_alpha behind t and of dhT."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import linear_attn as O
+from tests._attn import TOL, attn_case, decay_bound, upstream
+from tests._layers import BF16, FP32, cuda, say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gdr():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from gated_delta_rule_70_amd import binding
+    binding.lib()
+    return binding
+
+
+def reached(which, t, T):
+    """tokens of dq, dk, dv and dlog_alpha, and whether dh0, that a bad token t of an input may reach"""
+    at, on, behind, before, to, none, every = [t], range(t, T), range(t + 1, T), range(t), range(t + 1), [], range(T)
+    return {"q": (none, to, to, to, True), "k": (on, none, at, behind, False), "v": (on, at, none, behind, False),
+            "log_alpha": (on, before, before, every, True), "dout": (at, to, to, to, True),
+            "h0": (every, none, none, every, False), "dhT": (none, every, every, every, True)}[which]
+
+
+SIZES = [(64, 64, 64, False), (300, 64, 96, False), (700, 64, 64, False), (1100, 128, 64, True)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("T,dk,dv,packed", SIZES)
+@pytest.mark.parametrize("which", ["q", "log_alpha", "dout", "h0", "dhT"])
+def test_a_bad_token(gdr, which, T, dk, dv, packed, dtype):
+    """One row of one head of the first sequence: other heads, the other sequence and all gradients whose formula does not hold the
+    row keep their bits; the gradients of the decays up to a bad key or value keep their value (they come another way then)."""
+    say("bad %s T %d dk %d dv %d %s" % (which, T, dk, dv, dtype))
+    lens = [T, 70] if packed else [T, T]
+    case = attn_case(lens, 2, 2, dk, dv, dtype, 800 + T + dk + dv, packed)
+    dout, dhT = upstream(case, 801)
+    q, k, v, la, h, cu = cuda(case)
+    given = dict(q=q, k=k, v=v, log_alpha=la, dout=dout.cuda(), h0=h, dhT=dhT.cuda())
+    back = lambda a: gdr.linear_attn_bwd(a["q"], a["k"], a["v"], a["log_alpha"], a["dout"], a["h0"], cu, a["dhT"])
+    clean = back(given)
+    ref = O.grads(*case[:4], dout, case[4], case[5], dhT)
+    bound = decay_bound(case, dout, dhT, ref, dtype, 4096)
+    for bad in (float("nan"), float("inf")):
+        if which == "log_alpha" and bad > 0:
+            continue  # not a decay
+        for t in ([0] if which in ("h0", "dhT") else [0, 5, T // 2 + 3, T - 1]):
+            moved = dict(given)
+            moved[which] = given[which].clone()
+            moved[which][(0, 1, 3, 2) if which in ("h0", "dhT") else (0, 1, t)] = bad
+            got = back(moved)
+            *rows, state = reached(which, t, T)
+            for i, (x, c) in enumerate(zip(got, clean)):
+                x, c = x.clone(), c.clone()
+                if i == 4:
+                    if state:
+                        assert not torch.isfinite(x[0, 1]).all()
+                        x[0, 1] = c[0, 1]
+                else:
+                    hit = list(rows[i])
+                    if hit:
+                        assert not torch.isfinite(x[0, 1, hit].flatten(1) if i < 3 else x[0, 1, hit][:, None]).all(1).any(), (i, t)
+                    if i == 3 and which in ("k", "v"):
+                        # H before t and G from t on, by recurrences of at most T steps, 2^-24 off a step and independently
+                        part = lambda z, lo, hi: z[:1, 1:, lo:hi].double()
+                        _, H = O.forward(*(part(z, 0, t) for z in case[:4]), case[4][:1, 1:])
+                        later = [part(z, t, T).clone() for z in case[:4]]
+                        later[3][:, :, 0] = 0.0  # (not the token's own decay)
+                        G = O.grads(*later, part(dout, t, T), None, None, dhT[:1, 1:].double())[4]
+                        one = T ** 0.5 * 2 ** -24 * np.linalg.norm(H) * np.linalg.norm(G)
+                        off = np.linalg.norm(x[0, 1, :t + 1].double().cpu().numpy() - ref[3][0, 1, :t + 1])
+                        assert off <= bound + (t + 1) ** 0.5 * one, (t, off, bound, one)
+                        hit = range(T)
+                    x[0, 1, list(hit)] = c[0, 1, list(hit)]
+                assert torch.equal(x, c), (bad, t, i)
