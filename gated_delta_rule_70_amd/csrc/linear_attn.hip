@@ -789,9 +789,68 @@ struct DecayGrad {
     float *dla;                  // [B][Hv][T]
     double *part;                // [slots][Hv]: the slot's sum, where a head has one decay
     int elems;
+    // for tokens that are not finite: the inputs, and the states that enter the segments (with a split by slot) from both sides
+    const void *q, *k, *v, *dout;
+    const float *before, *behind;
+    int dk, dv;
+    bool split;
 };
 
-// A workgroup takes a segment of a head. The sums run over up to thousands of tokens and cancel: they are held in 64 bits.
+template <typename E>
+__device__ __forceinline__ bool finite_row(const E *p, int n) {
+    bool all = true;
+    for (int i = 0; i < n; ++i) all = all && finite((float)p[i]);
+    return all;
+}
+
+// The gradient at the segment's first token whose key or value is not finite: alpha_t <G_t, H_{t-1}>, where neither G nor H holds
+// that token's key and value, from the recurrences themselves. Returns the token, or -1 where there is none, or where a query or
+// an output's gradient from it on is not finite either, which every token up to it holds.
+template <typename E>
+__device__ __forceinline__ int first_bad(const AttnArgs &a, const DecayGrad &d, const Span &sp, unsigned head, double *held, double &grad) {
+    __shared__ int bounds[2];
+    const int tid = threadIdx.x;
+    const unsigned kh = head / a.group;
+    const int64_t keys = (sp.row * a.Hk + kh) * a.T + sp.t0, values = (sp.row * a.Hv + head) * a.T + sp.t0;
+    const E *q = reinterpret_cast<const E *>(d.q) + keys * d.dk, *k = reinterpret_cast<const E *>(d.k) + keys * d.dk;
+    const E *v = reinterpret_cast<const E *>(d.v) + values * d.dv, *dout = reinterpret_cast<const E *>(d.dout) + values * d.dv;
+    if (tid == 0) {
+        bounds[0] = sp.hi;
+        bounds[1] = -1;
+    }
+    __syncthreads();
+    int first = sp.hi, last = -1;
+    for (int t = sp.lo + tid; t < sp.hi; t += 256) {
+        const int64_t tk = (int64_t)t * d.dk, tv = (int64_t)t * d.dv;
+        if (first == sp.hi && !(finite_row(k + tk, d.dk) && finite_row(v + tv, d.dv))) first = t;
+        if (!(finite_row(q + tk, d.dk) && finite_row(dout + tv, d.dv))) last = t;
+    }
+    if (first < sp.hi) atomicMin(&bounds[0], first);
+    if (last >= 0) atomicMax(&bounds[1], last);
+    __syncthreads();
+    const int bad = bounds[0];
+    if (bad == sp.hi || bounds[1] >= bad) return -1;
+    auto alpha = [&](int t) {
+        const float la = a.la_token ? a.la[values + t] : a.la[head];
+        return ex2((float)((double)(la < kLeast ? kLeast : la) * kLog2e));
+    };
+    const int64_t from = (int64_t)(d.split ? sp.slot : sp.seq) * a.Hv + head;
+    double sum = 0.;
+    for (int e = tid; e < d.elems; e += 256) {
+        const int r = e / d.dv, c = e % d.dv;
+        float h = d.before ? d.before[from * d.elems + e] : 0.f, g = d.behind ? d.behind[from * d.elems + e] : 0.f;
+        for (int t = sp.lo; t < bad; ++t) h = alpha(t) * h + (float)k[(int64_t)t * d.dk + r] * (float)v[(int64_t)t * d.dv + c];
+        for (int t = sp.hi - 1; t > bad; --t) g = alpha(t) * (g + (float)q[(int64_t)t * d.dk + r] * (float)dout[(int64_t)t * d.dv + c]);
+        g += (float)q[(int64_t)bad * d.dk + r] * (float)dout[(int64_t)bad * d.dv + c];
+        sum += (double)g * h;
+    }
+    grad = alpha(bad) * sum_all(sum, held);
+    return bad;
+}
+
+// A workgroup takes a segment of a head. The sums run over up to thousands of tokens and cancel: they are held in 64 bits. The sums hold each later token's q . dq and k . dk,
+// where a bad key or value would reach all earlier tokens, which do not depend on it: such a segment's are taken again up to there.
+template <typename E>
 __global__ __launch_bounds__(256) void decay_grad_kernel(AttnArgs a, DecayGrad d) {
     __shared__ double held[4], waves[4];
     const unsigned id = (unsigned)block_id(), slot = id / (unsigned)a.Hv, head = id % (unsigned)a.Hv;
@@ -814,18 +873,36 @@ __global__ __launch_bounds__(256) void decay_grad_kernel(AttnArgs a, DecayGrad d
             carry = sum_all(carry, held);
         }
         const int64_t base = ((int64_t)sp.row * a.Hv + head) * a.T + sp.t0;
-        for (int end = sp.hi; end > sp.lo; end -= 256) {
-            const int t = end - 1 - tid;  // thread 0 has the last token
-            double v = lane_sums(t >= sp.lo ? (double)d.dq_dot[base + t] - (double)d.dk_dot[base + t] : 0.);
-            __syncthreads();
-            if (lane == 63) waves[wave] = v;
-            __syncthreads();
-            v += carry;
-            for (int w = 0; w < wave; ++w) v += waves[w];
-            carry += waves[0] + waves[1] + waves[2] + waves[3];
-            if (t >= sp.lo) {
-                if (a.la_token) d.dla[base + t] = (float)v;
-                else sum += v;
+        // the tokens before `end`, behind which the sum is `carry`; whether all sums were finite
+        auto walk = [&](int end, double carry) {
+            bool fine = true;
+            for (; end > sp.lo; end -= 256) {
+                const int t = end - 1 - tid;  // thread 0 has the last token
+                double v = lane_sums(t >= sp.lo ? (double)d.dq_dot[base + t] - (double)d.dk_dot[base + t] : 0.);
+                __syncthreads();
+                if (lane == 63) waves[wave] = v;
+                __syncthreads();
+                v += carry;
+                for (int w = 0; w < wave; ++w) v += waves[w];
+                carry += waves[0] + waves[1] + waves[2] + waves[3];
+                if (t >= sp.lo) {
+                    fine = fine && finite((float)v);
+                    if (a.la_token) d.dla[base + t] = (float)v;
+                    else sum += v;
+                }
+            }
+            return fine;
+        };
+        if (__builtin_expect(__syncthreads_or(!walk(sp.hi, carry)), 0)) {
+            double grad;
+            const int bad = first_bad<E>(a, d, sp, head, held, grad);
+            if (bad >= 0) {
+                if (a.la_token) {
+                    if (tid == 0) d.dla[base + bad] = (float)grad;
+                } else {
+                    sum = tid ? 0. : bad + 1 < sp.hi ? __builtin_nan("") : grad;  // (tokens behind it hold it)
+                }
+                walk(bad, grad);
             }
         }
     }
@@ -1059,9 +1136,10 @@ hipError_t bwd(const AttnCall &c, hipStream_t s) {
         e = sweep<E, kResults>(a, 2, 1, s);
         if (e != hipSuccess) return e;
     }
-    const DecayGrad d{p.seg ? ends : nullptr, last, c.dhT, at(w.dq_dot), at(w.dk_dot), c.dla, reinterpret_cast<double *>(c.ws + w.part), dk * dv};
+    const DecayGrad d{p.seg ? ends : nullptr, last, c.dhT, at(w.dq_dot), at(w.dk_dot), c.dla, reinterpret_cast<double *>(c.ws + w.part), dk * dv,
+                      c.q, c.k, c.v, c.dout, p.seg ? states : c.h0, p.seg ? back : c.dhT, dk, dv, p.seg != 0};
     if (p.slots) {
-        hipLaunchKernelGGL(decay_grad_kernel, grid_of(p.slots * c.Hv, 256), dim3(256), 0, s, a, d);
+        hipLaunchKernelGGL((decay_grad_kernel<E>), grid_of(p.slots * c.Hv, 256), dim3(256), 0, s, a, d);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

@@ -613,7 +613,8 @@ gdr_status_t gdr_linear_ce_bwd(const void *x, const void *w, const int64_t *targ
  *
  * Every sum is held in fp32 or more, and what is formed from the inputs on the way enters the matrix
  * products with 24 bits: of bf16 tensors only out and the gradients of q, k and v are rounded to
- * bf16, once. NaN and infinities of a token reach no earlier one. Tokens before cu_seqlens[0] and behind
+ * bf16, once. NaN and infinities of a token reach no earlier token's output, and of the gradients those alone whose formula
+ * (dlog_alpha_t = alpha_t <G_t, H_{t-1}> with the adjoint state G) holds them. Tokens before cu_seqlens[0] and behind
  * cu_seqlens[num_seqs] belong to no sequence: they are not read, and their rows of the results are not written.
  * Calls that share a workspace must not overlap.
  *

@@ -38,7 +38,7 @@ SIZES = [(64, 64, 64, False), (300, 64, 96, False), (700, 64, 64, False), (1100,
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("T,dk,dv,packed", SIZES)
-@pytest.mark.parametrize("which", ["q", "log_alpha", "dout", "h0", "dhT"])
+@pytest.mark.parametrize("which", ["q", "k", "v", "log_alpha", "dout", "h0", "dhT"])
 def test_a_bad_token(gdr, which, T, dk, dv, packed, dtype):
     """One row of one head of the first sequence: other heads, the other sequence and all gradients whose formula does not hold the
     row keep their bits; the gradients of the decays up to a bad key or value keep their value (they come another way then)."""
@@ -84,3 +84,38 @@ def test_a_bad_token(gdr, which, T, dk, dv, packed, dtype):
                         hit = range(T)
                     x[0, 1, list(hit)] = c[0, 1, list(hit)]
                 assert torch.equal(x, c), (bad, t, i)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("T", [90, 700])
+def test_one_decay_a_head(gdr, T, dtype):
+    """A bad value of the last token alone: the head's gradient is the sum of finite ones."""
+    case = attn_case([T], 2, 2, 64, 64, dtype, 860, decay="head")
+    dout, _ = upstream(case, 861)
+    q, k, v, la, h, _ = cuda(case)
+    ref = O.grads(*case[:4], dout, case[4])
+    for t, whole in ((T - 1, True), (T - 2, False)):
+        moved = v.clone()
+        moved[0, 1, t] = float("nan")
+        got = gdr.linear_attn_bwd(q, k, moved, la, dout.cuda(), h)[3]
+        assert torch.isfinite(got).tolist() == [True, whole]
+        if whole:
+            assert np.linalg.norm(got.double().cpu().numpy() - ref[3]) <= 2 * decay_bound(case, dout, None, ref, dtype, 4096)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("T", [90, 700])
+def test_shared_heads(gdr, T, dtype):
+    """A bad value head: the key head's gradients of the queries from there on and of that key, nothing else of other value heads."""
+    case = attn_case([T], 1, 3, 64, 64, dtype, 870)
+    dout, dhT = upstream(case, 871)
+    q, k, v, la, h, _ = cuda(case)
+    args = lambda v: (q, k, v, la, dout.cuda(), h, None, dhT.cuda())
+    clean, t = gdr.linear_attn_bwd(*args(v)), 37
+    moved = v.clone()
+    moved[0, 1, t] = float("nan")
+    got = gdr.linear_attn_bwd(*args(moved))
+    assert torch.equal(got[0][:, :, :t], clean[0][:, :, :t]) and torch.isnan(got[0][:, :, t:]).all()
+    assert torch.isnan(got[1][:, :, t]).all() and torch.equal(torch.cat([got[1][:, :, :t], got[1][:, :, t + 1:]], 2), torch.cat([clean[1][:, :, :t], clean[1][:, :, t + 1:]], 2))
+    assert torch.equal(got[2], clean[2]) and torch.equal(got[4], clean[4])
+    assert torch.equal(got[3][:, [0, 2]], clean[3][:, [0, 2]]) and torch.isfinite(got[3][:, 1, :t + 1]).all() and torch.isnan(got[3][:, 1, t + 1:]).all()
