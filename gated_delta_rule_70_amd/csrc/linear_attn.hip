@@ -848,7 +848,8 @@ __device__ __forceinline__ int first_bad(const AttnArgs &a, const DecayGrad &d, 
     return bad;
 }
 
-// A workgroup takes a segment of a head. The sums run over up to thousands of tokens and cancel: they are held in 64 bits. The sums hold each later token's q . dq and k . dk,
+// A workgroup takes a segment of a head. The sums run over up to thousands of tokens and cancel: they are held in 64 bits. A
+// decay of nothing left has no gradient, whatever the sums leave of theirs. The sums hold each later token's q . dq and k . dk,
 // where a bad key or value would reach all earlier tokens, which do not depend on it: such a segment's are taken again up to there.
 template <typename E>
 __global__ __launch_bounds__(256) void decay_grad_kernel(AttnArgs a, DecayGrad d) {
@@ -878,6 +879,7 @@ __global__ __launch_bounds__(256) void decay_grad_kernel(AttnArgs a, DecayGrad d
             bool fine = true;
             for (; end > sp.lo; end -= 256) {
                 const int t = end - 1 - tid;  // thread 0 has the last token
+                const float la = t < sp.lo ? 0.f : a.la_token ? a.la[base + t] : a.la[head];
                 double v = lane_sums(t >= sp.lo ? (double)d.dq_dot[base + t] - (double)d.dk_dot[base + t] : 0.);
                 __syncthreads();
                 if (lane == 63) waves[wave] = v;
@@ -887,6 +889,7 @@ __global__ __launch_bounds__(256) void decay_grad_kernel(AttnArgs a, DecayGrad d
                 carry += waves[0] + waves[1] + waves[2] + waves[3];
                 if (t >= sp.lo) {
                     fine = fine && finite((float)v);
+                    if (la <= kLeast) v *= 0.;
                     if (a.la_token) d.dla[base + t] = (float)v;
                     else sum += v;
                 }

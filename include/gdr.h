@@ -640,6 +640,9 @@ gdr_status_t gdr_linear_ce_bwd(const void *x, const void *w, const int64_t *targ
  *   dh0         [S][Hv][dk][dv] fp32, or NULL when not wanted
  *   workspace   at least gdr_linear_attn_bwd_workspace_bytes(dims, packed) bytes
  *
+ * dlog_alpha is taken from sums over the sequence's later tokens (4096 at most) which cancel: it is good to fp32's rounding of
+ * those sums' terms, not of itself, which is less where decays are strong. Where alpha is 0 it is 0.
+ *
  * gdr_linear_attn_step - one token of N sequences: q, k [N][Hk][dk], v, out [N][Hv][dv], log_alpha [N][Hv] or
  * [Hv], state_in, state_out [N][Hv][dk][dv] fp32 (state_out may be exactly state_in).
  *

@@ -119,3 +119,21 @@ def test_shared_heads(gdr, T, dtype):
     assert torch.isnan(got[1][:, :, t]).all() and torch.equal(torch.cat([got[1][:, :, :t], got[1][:, :, t + 1:]], 2), torch.cat([clean[1][:, :, :t], clean[1][:, :, t + 1:]], 2))
     assert torch.equal(got[2], clean[2]) and torch.equal(got[4], clean[4])
     assert torch.equal(got[3][:, [0, 2]], clean[3][:, [0, 2]]) and torch.isfinite(got[3][:, 1, :t + 1]).all() and torch.isnan(got[3][:, 1, t + 1:]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("T", [130, 900])
+def test_decays_that_leave_nothing(gdr, T, dtype):
+    """alpha of 0 to the last bit of fp32 has a gradient of 0, whatever the sums it is taken from."""
+    case = attn_case([T], 1, 2, 64, 64, dtype, 880)
+    dout, dhT = upstream(case, 881)
+    q, k, v, la, h, _ = cuda(case)
+    for least in (float("-inf"), -1e30, -500.0, -104.0):
+        cut = la.clone()
+        cut[0, 0, 70:73], cut[0, 1, T - 1] = least, least
+        got = gdr.linear_attn_bwd(q, k, v, cut, dout.cuda(), h, None, dhT.cuda())[3]
+        assert not got[0, 0, 70:73].any() and got[0, 1, T - 1] == 0
+        assert got[0, 0, :70].all() and got[0, 0, 73:].all()
+    head = torch.tensor([float("-inf"), -0.1], device="cuda")
+    got = gdr.linear_attn_bwd(q, k, v, head, dout.cuda(), h, None, dhT.cuda())[3]
+    assert got[0] == 0 and got[1] != 0
