@@ -65,10 +65,12 @@ struct AttnRole {
     const void *other;   // like out: each row's product with out's goes to dot, [B][Hv][T], if that is wanted
     float *dot;
     const float *s_in;   // entering states by slot (in_slots) or sequence, or null for zeros
-    float *s_out;        // states that sequences end with; without outputs, the segments' own, by slot
-    float *decay;        // without outputs: the segments' decays [slots][Hv]
+    const float *s_cuts;  // with cuts: the states that go over them, turned (s_in is for the sequences' first segments)
+    float *s_out;        // states that sequences end with; without outputs, the segments' own, by slot (cut)
+    float *decay;        // without outputs: the segments' decays [slots (cuts)][Hv]
     int32_t da, db;
     bool xk, yk, zk, ok, reverse, in_turned, out_turned, in_slots;  // *_turned: the state is stored as [db][da]
+    bool cuts;           // forwards: states between segments lie by cut, and only the segments before one have a state of their own
     bool shares;         // mixed form: out is fp32
 };
 
@@ -78,9 +80,10 @@ struct AttnArgs {
     const int32_t *cu;
     int64_t B, T, Hk, Hv, nseq;
     int64_t seg, per_seq, slots, slices;  // seg 0: slots are sequences
-    bool la_token, skip_last;             // skip_last: without outputs, the segment that no other one follows is left out
+    int64_t cuts;                         // where a sequence may be cut: slots without the sequences
+    bool la_token;
     uint32_t group;                       // value heads of a key head
-    Divisor by_inner, by_roles, by_slices, by_Hk, by_per, by_seg;
+    Divisor by_inner, by_roles, by_slices, by_Hk, by_per, by_cuts, by_seg;
 };
 
 // A call of linear attention: forward, backward or step (x, y, z of the roles unused).

@@ -185,9 +185,25 @@ struct Span {
 };
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
+// The last of n sequences whose key is not past `at` (the first one if all are), by all lanes of a wave at once.
+template <typename Key>
+__device__ __forceinline__ unsigned last_up_to(unsigned at, unsigned n, Key key) {
+    const unsigned lane = threadIdx.x & 63;
+    unsigned lo = 0;
+    while (n > 1) {
+        const unsigned step = (n + 63) / 64, on = lane * step;
+        const unsigned m = (unsigned)__popcll(__ballot(on < n && key(lo + on) <= at)), skip = m > 1 ? (m - 1) * step : 0;
+        lo += skip;
+        n = n - skip < step ? n - skip : step;
+    }
+    return (unsigned)uniform((int)lo);
+}
+
 // Slots are segments of a.seg tokens; without a split (a.seg 0) slots are sequences. Packed: the segments of sequence s begin at
-// slot cu[s] / seg + s. Boundaries are held inside the row whatever cu_seqlens has.
-__device__ __forceinline__ Span span_of(const AttnArgs &a, unsigned slot) {
+// slot cu[s] / seg + s. Cuts are where a segment ends and its sequence goes on: those of sequence s begin at cut cu[s] / seg (s
+// (per_seq - 1) if not packed), so that slot i of sequence s lies between cuts i - s - 1 and i - s. With `cut`, the segment before
+// a cut is asked for. Boundaries are held inside the row whatever cu_seqlens has.
+__device__ __forceinline__ Span span_of(const AttnArgs &a, unsigned slot, bool cut = false) {
     Span p;
     const unsigned seg = (unsigned)a.seg;
     const int T = (int)a.T;
@@ -195,20 +211,16 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, unsigned slot) {
     unsigned piece = 0;
     p.slot = (int)slot;
     if (!a.cu) {
-        const unsigned s = a.by_per(slot);  // (one segment a sequence without a split)
+        const Divisor &by = cut ? a.by_cuts : a.by_per;  // (one segment a sequence without a split)
+        const unsigned s = by(slot);
         p.seq = p.row = (int)s;
-        piece = slot - s * a.by_per.d;
+        piece = slot - s * by.d;
     } else {
         unsigned s = slot;
         if (seg) {
-            unsigned above = (unsigned)a.nseq;  // the last s whose first slot is not past this one
-            s = 0;
-            while (above - s > 1) {
-                const unsigned mid = (above + s) / 2;
-                if (a.by_seg((unsigned)uniform(a.cu[mid])) + mid <= slot) s = mid;
-                else above = mid;
-            }
-            piece = slot - (a.by_seg((unsigned)uniform(a.cu[s])) + s);
+            // whose first slot or cut is not past this one
+            s = last_up_to(slot, (unsigned)a.nseq, [&](unsigned i) { return a.by_seg((unsigned)a.cu[i]) + (cut ? 0 : i); });
+            piece = slot - (a.by_seg((unsigned)uniform(a.cu[s])) + (cut ? 0 : s));
         }
         p.seq = (int)s;
         p.row = 0;
@@ -220,7 +232,7 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, unsigned slot) {
     p.t0 = from;
     p.len = end - from;
     const int64_t lo = (int64_t)piece * seg;
-    p.some = piece == 0 || lo < p.len;
+    p.some = cut ? lo + seg < p.len : piece == 0 || lo < p.len;
     p.lo = p.some ? (int)lo : 0;
     p.hi = seg && (int64_t)p.lo + seg < p.len ? p.lo + (int)seg : p.len;
     return p;
@@ -328,9 +340,12 @@ __global__ __launch_bounds__(NW * 64, DA > 128 ? 1 : NW / 2) void sweep_kernel(A
     const unsigned in = at - round * a.by_inner.d, unit = a.by_roles(in), member = a.by_slices(unit), slot = a.by_Hk(outer);
     const AttnRole &r = a.roles[first_role + (in - unit * a.by_roles.d)];
     const unsigned slice = unit - member * a.by_slices.d, kh = outer - slot * Hk, head = kh * a.group + member;
-    const Span sp = span_of(a, slot);
+    const Span sp = span_of(a, slot, !OUT && r.cuts);
     if (!sp.some) return;
-    if (!OUT && a.skip_last && (r.reverse ? sp.first() : sp.last())) return;
+    // the cut before a segment that a state enters over
+    const bool over = OUT && r.cuts && !sp.first();
+    const unsigned before = (unsigned)(sp.slot - sp.seq - 1);
+    if (over && before >= a.cuts) return;  // (boundaries that are none)
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
     const int wave = uniform(tid >> 6);
@@ -399,9 +414,10 @@ __global__ __launch_bounds__(NW * 64, DA > 128 ? 1 : NW / 2) void sweep_kernel(A
     for (int t = 0; t < TA; ++t)
 #pragma unroll
         for (int n = 0; n < NT; ++n) h[t][n] = zero4();
-    if (OUT && r.s_in && active) {
-        const float *p = r.s_in + ((int64_t)(r.in_slots ? sp.slot : sp.seq) * Hv + head) * da * db;
-        if (r.in_turned) {
+    const float *s_in = over ? r.s_cuts : r.s_in;
+    if (OUT && s_in && active) {
+        const float *p = s_in + ((int64_t)(over ? (int)before : r.in_slots ? sp.slot : sp.seq) * Hv + head) * da * db;
+        if (over || r.in_turned) {
 #pragma unroll
             for (int t = 0; t < TA; ++t)
 #pragma unroll
@@ -709,7 +725,8 @@ __device__ __forceinline__ double sum_all(double v, double *held) {
     return held[0] + held[1] + held[2] + held[3];
 }
 
-// Four elements of one head's state a thread: each segment's own state is replaced by the one that enters it. States are
+// Four elements of one head's state a thread: each segment's own state is replaced by the one that enters it, or, with `cuts` (whose
+// first one of a sequence names the workgroup), that of the segment before each cut by the one that goes over it. States are
 // [rows][cols] here, init and last the same or, turned, [cols][rows]. With `ends` (backwards, behind the forward's states), each
 // workgroup leaves its part of <the adjoint that enters segment i from behind, the state there>, which enters segment i + 1.
 struct Join {
@@ -719,24 +736,33 @@ struct Join {
     const float *other, *other_last;
     double *ends;  // [slots][Hv][blocks of a state]
     int rows, cols;
-    bool turned, reverse;
+    bool turned, reverse, cuts;
 };
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Join j) {
     __shared__ double held[4];
     const int64_t elems = (int64_t)j.rows * j.cols;
     const unsigned blocks = (unsigned)(elems / 1024), id = (unsigned)block_id(), unit = id / blocks, block = id % blocks;
-    const unsigned seq = unit / (unsigned)a.Hv, head = unit % (unsigned)a.Hv;
-    if (seq >= a.nseq) return;
+    const unsigned which = unit / (unsigned)a.Hv, head = unit % (unsigned)a.Hv;
+    if (which >= (j.cuts ? a.cuts : a.nseq)) return;
     const int64_t e = block * 1024 + threadIdx.x * 4;
-    int first = (int)(seq * a.per_seq), n = (int)a.per_seq;
-    if (a.cu) {
+    unsigned seq = which;
+    int first = (int)(which * a.per_seq), n = (int)a.per_seq;
+    if (j.cuts) {
+        const Span sp = span_of(a, which, true);
+        if (!sp.some || !sp.first()) return;
+        seq = (unsigned)sp.seq;
+        first = (int)which;
+        n = (sp.len - 1) / (int)a.seg;
+        if ((int64_t)first + n > a.cuts) return;  // boundaries that are none
+    } else if (a.cu) {
         const int from = a.cu[seq], len = a.cu[seq + 1] - from;
         first = (int)(a.by_seg((unsigned)from) + seq);
         n = len > a.seg ? (int)((len + a.seg - 1) / a.seg) : 1;
         if (first < 0 || (int64_t)first + n > a.slots) return;  // boundaries that are none
     }
     const int row = (int)(e / j.cols), col = (int)(e % j.cols);
-    auto outside = [&](int i) { return unit * elems + (j.turned ? (int64_t)(col + i) * j.rows + row : e + i); };
+    const int64_t at = ((int64_t)seq * a.Hv + head) * elems;
+    auto outside = [&](int i) { return at + (j.turned ? (int64_t)(col + i) * j.rows + row : e + i); };
     floatx4 h = zero4();
     if (j.init) {
 #pragma unroll
@@ -751,13 +777,13 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Join j) {
         for (int p = 0; p < kAhead; ++p) {
             s[p] = x[p] = zero4();
             d[p] = 0.f;
-            if (i + p + 1 < n || (i + p < n && j.last)) {
+            if (i + p + 1 < n || (i + p < n && (j.last || j.cuts))) {
                 s[p] = *reinterpret_cast<const floatx4 *>(j.states + (slot(i + p) * a.Hv + head) * elems + e);
                 d[p] = j.decays[slot(i + p) * a.Hv + head];
             }
             if (j.ends && i + p < n) {
                 if (i + p > 0) x[p] = *reinterpret_cast<const floatx4 *>(j.other + ((slot(i + p) + 1) * a.Hv + head) * elems + e);
-                else if (j.other_last) x[p] = *reinterpret_cast<const floatx4 *>(j.other_last + unit * elems + e);
+                else if (j.other_last) x[p] = *reinterpret_cast<const floatx4 *>(j.other_last + at + e);
             }
         }
 #pragma unroll
@@ -770,8 +796,9 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Join j) {
                     v = sum_all(v, held);
                     if (threadIdx.x == 0) j.ends[(slot(i + p) * a.Hv + head) * blocks + block] = v;
                 }
-                *reinterpret_cast<floatx4 *>(j.states + (slot(i + p) * a.Hv + head) * elems + e) = h;
-                h = d[p] * h + s[p];
+                const floatx4 next = d[p] * h + s[p];
+                *reinterpret_cast<floatx4 *>(j.states + (slot(i + p) * a.Hv + head) * elems + e) = j.cuts ? next : h;
+                h = next;
             }
     }
     if (j.last) {
@@ -991,7 +1018,7 @@ __global__ __launch_bounds__(256) void step_kernel(AttnCall a) {
 template <typename E, int DA, int NT, Form F>
 hipError_t sweep_t(AttnArgs a, int first, int n, hipStream_t s) {
     constexpr int NW = 4;
-    const int64_t outer = a.slots * a.Hk, inner = n * a.slices * a.group;
+    const int64_t outer = (F == kStates && a.roles[first].cuts ? a.cuts : a.slots) * a.Hk, inner = n * a.slices * a.group;
     if (outer == 0) return hipSuccess;
     a.by_inner = Divisor(inner);
     a.by_roles = Divisor(n);
@@ -1006,7 +1033,7 @@ hipError_t sweep(AttnArgs a, int first, int n, hipStream_t s) {
     const AttnRole &r = a.roles[first];
     // (the results' products with q and k are formed by the one workgroup that has all columns)
     const bool narrow = F == kStates || F == kResults;
-    const int nt = narrow ? attn_tiles(r.db, a.slots * a.Hv * n * attn_slices(r.db)) : attn_tiles(r.db);
+    const int nt = narrow ? attn_tiles(r.db, (r.cuts && F == kStates ? a.cuts : a.slots) * a.Hv * n * attn_slices(r.db)) : attn_tiles(r.db);
     a.slices = attn_slices(r.db, nt);
     if (r.da <= 64) return nt == 1 ? sweep_t<E, 64, 1, F>(a, first, n, s) : sweep_t<E, 64, 2, F>(a, first, n, s);
     if (r.da <= 128) return nt == 1 ? sweep_t<E, 128, 1, F>(a, first, n, s) : sweep_t<E, 128, 2, F>(a, first, n, s);
@@ -1016,7 +1043,7 @@ hipError_t sweep(AttnArgs a, int first, int n, hipStream_t s) {
 }
 
 hipError_t join(const AttnArgs &a, const Join &j, hipStream_t s) {
-    hipLaunchKernelGGL(join_kernel, grid_of(a.nseq * a.Hv * (j.rows * j.cols / 1024), 256), dim3(256), 0, s, a, j);
+    hipLaunchKernelGGL(join_kernel, grid_of((j.cuts ? a.cuts : a.nseq) * a.Hv * (j.rows * j.cols / 1024), 256), dim3(256), 0, s, a, j);
     return hipGetLastError();
 }
 
@@ -1025,11 +1052,12 @@ AttnArgs args_of(const AttnCall &c, const AttnPlan &p) {
     a.la = c.la;
     a.cu = c.cu;
     a.B = c.B; a.T = c.T; a.Hk = c.Hk; a.Hv = c.Hv; a.nseq = c.nseq;
-    a.seg = p.seg; a.per_seq = p.per_seq; a.slots = p.slots;
+    a.seg = p.seg; a.per_seq = p.per_seq; a.slots = p.slots; a.cuts = p.slots - c.nseq;
     a.la_token = c.la_token;
     a.group = (uint32_t)(c.Hv / c.Hk);
     a.by_Hk = Divisor(c.Hk);
     a.by_per = Divisor(p.per_seq);
+    a.by_cuts = Divisor(p.per_seq > 1 ? p.per_seq - 1 : 1);
     a.by_seg = Divisor(p.seg ? p.seg : 1);
     return a;
 }
@@ -1049,17 +1077,15 @@ hipError_t fwd(const AttnCall &c, hipStream_t s) {
         r.s_out = states;
         r.decay = decays;
         r.out_turned = true;  // a lane of the sweep then reads 16 bytes at a time
-        a.skip_last = true;
+        r.cuts = true;
         hipError_t e = sweep<E, kStates>(a, 0, 1, s);
         if (e != hipSuccess) return e;
-        e = join(a, Join{states, decays, c.h0, nullptr, nullptr, nullptr, nullptr, dv, dk, true, false}, s);
+        e = join(a, Join{states, decays, c.h0, nullptr, nullptr, nullptr, nullptr, dv, dk, true, false, true}, s);
         if (e != hipSuccess) return e;
-        r.s_in = states;
-        r.in_slots = r.in_turned = true;
+        r.s_cuts = states;
         r.out_turned = false;
-    } else {
-        r.s_in = c.h0;
     }
+    r.s_in = c.h0;
     r.out = c.out;
     r.s_out = c.hT;
     return sweep<E, kResults>(a, 0, 1, s);
@@ -1089,9 +1115,9 @@ hipError_t bwd(const AttnCall &c, hipStream_t s) {
         b.reverse = true;
         e = sweep<E, kStates>(a, 0, 2, s);
         if (e != hipSuccess) return e;
-        e = join(a, Join{states, decays, c.h0, c.dhT ? last : nullptr, nullptr, nullptr, nullptr, dk, dv, false, false}, s);
+        e = join(a, Join{states, decays, c.h0, c.dhT ? last : nullptr, nullptr, nullptr, nullptr, dk, dv, false, false, false}, s);
         if (e != hipSuccess) return e;
-        e = join(a, Join{back, back_decays, c.dhT, c.dh0, states, c.dhT ? last : nullptr, ends, dk, dv, false, true}, s);
+        e = join(a, Join{back, back_decays, c.dhT, c.dh0, states, c.dhT ? last : nullptr, ends, dk, dv, false, true, false}, s);
         if (e != hipSuccess) return e;
     }
     AttnRole &q = a.roles[0], &k = a.roles[1], &v = a.roles[2];

@@ -1,0 +1,37 @@
+"""How linear attention cuts sequences, on the host: what one workgroup may have to walk, whatever the lengths of packed sequences
+are, and what is not worth a cut."""
+from __future__ import annotations
+
+import os
+import shutil
+import subprocess
+
+import pytest
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+CXX = shutil.which("g++")
+pytestmark = pytest.mark.skipif(CXX is None, reason="no host C++ compiler")
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    exe = str(tmp_path_factory.mktemp("plan") / "driver")
+    subprocess.run([CXX, "-O1", "-std=c++17", "-Wall", os.path.join(HERE, "attn_plan_driver.cpp"), "-o", exe], check=True)
+
+    def answer(T, nseq, units, packed, backward):
+        out = subprocess.run([exe], input="plan %d %d %d %d %d\n" % (T, nseq, units, packed, backward), capture_output=True, text=True, check=True).stdout
+        return [int(w) for w in out.split()]
+
+    return answer
+
+
+@pytest.mark.parametrize("units", [1, 8, 16, 100])
+@pytest.mark.parametrize("nseq", [2, 10, 63, 64, 65, 300, 2000])
+@pytest.mark.parametrize("T", [300, 2049, 20000, 131072])
+def test_one_long_sequence_among_many(plan, T, nseq, units):
+    """Nearly all packed tokens may be one sequence's: no workgroup walks more than its heads' share of the card, 2048 tokens, or
+    4096 backwards, unless the sequences are shorter than a chunk in the mean."""
+    share = -(-T * units // 512)
+    for backward, most in ((0, 2048), (1, 4096)):
+        seg, _, _ = plan(T, nseq, units, 1, backward)
+        assert (seg or T) <= max(most, share + 63) or (not backward and T < 64 * nseq)
