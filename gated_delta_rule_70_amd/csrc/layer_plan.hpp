@@ -58,10 +58,14 @@ constexpr int kAttnChunk = 64;  // tokens of a bf16 chunk; fp32 chunks are half 
 struct AttnPlan {
     int64_t seg, per_seq, slots;
 };
-// `units`: workgroups of a whole sequence (heads and column slices). Split where whole sequences leave compute units idle (two
-// workgroups share one): fewer than 384 of them, or, packed, fewer than 1024 (their lengths differ and are not known here);
-// into about 512, of whole chunks. Up to 256 tokens one workgroup's few chunks take less than the two launches that a split
-// adds. The backward's segments end at 4096 tokens, since sums over them cancel.
+// `units`: workgroups of a whole sequence (heads and column slices). Split, into about 512 of whole chunks, where whole sequences
+// leave too many compute units idle to be worth less than the states' sweep and the second read: fewer than 192 of them, 96 in the
+// backward, which has each twice. Sequences of 4096 tokens of 16 heads of 128, bf16, split and whole: forward 8 of them (128) 239 and 289 us, 12 (192)
+// 404 and 385, 18 570 and 499, 23 894 and 531; backward 4 (64) 382 and 479, 6 (96) 640 and 577, 10 990 and 670; of 1024 tokens
+// forward 8 89 and 86, backward 4 149 and 132; forward fp32 4 316 and 497, 8 527 and 504. Up to 256 tokens one workgroup's few chunks take less
+// than the two launches that a split adds, or as long: 192 tokens of 16 heads 20 us whole and 23 split, 256 24 and 23, 320 28
+// and 24, backward 49 and 44. The backward's segments end at 4096 tokens, since sums over them cancel. Packed, fewer than
+// 1024 workgroups are split, since their lengths differ and are not known here.
 //
 // Packed sequences of 1024 workgroups and more: the forward cuts only those that are longer than their heads' share of the card,
 // for two launches that find nothing to do otherwise. 16 heads of 128: a document of 100,000 tokens among 63 of 500 takes 913 us so, 9289 whole; 3000
@@ -73,7 +77,7 @@ inline AttnPlan attn_plan(int64_t T, int64_t nseq, int64_t units, bool packed, b
     if (nseq == 0 || T <= 256) return p;
     int64_t seg = (rows * units + 511) / 512;
     seg = (seg + kAttnChunk - 1) / kAttnChunk * kAttnChunk;
-    if (packed ? nseq * units >= 1024 && (backward || T <= 2048 || T < kAttnChunk * nseq) : nseq * units >= 384) seg = T;
+    if (packed ? nseq * units >= 1024 && (backward || T <= 2048 || T < kAttnChunk * nseq) : nseq * units >= (backward ? 96 : 192)) seg = T;
     if (backward && seg > 4096) seg = 4096;
     if (seg >= T) return p;
     p.seg = seg;

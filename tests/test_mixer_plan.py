@@ -35,3 +35,20 @@ def test_one_long_sequence_among_many(plan, T, nseq, units):
     for backward, most in ((0, 2048), (1, 4096)):
         seg, _, _ = plan(T, nseq, units, 1, backward)
         assert (seg or T) <= max(most, share + 63) or (not backward and T < 64 * nseq)
+
+
+@pytest.mark.parametrize("T", [257, 1024, 4096])
+@pytest.mark.parametrize("nseq,units", [(12, 16), (23, 16), (3, 64), (1, 380), (383, 1)])
+def test_batches_that_fill_most_of_the_card_are_whole(plan, T, nseq, units):
+    assert plan(T, nseq, units, 0, 0) == [0, 1, nseq] and plan(T, nseq, units, 0, 1) == [0, 1, nseq]
+
+
+@pytest.mark.parametrize("backward,units", [(0, 8), (0, 128), (0, 191), (1, 8), (1, 64), (1, 95)])
+def test_fewer_are_cut(plan, backward, units):
+    seg, per, slots = plan(4096, 1, units, 0, backward)
+    assert 0 < seg <= 2048 and per == slots >= 2
+
+
+def test_backward_segments_end_where_sums_cancel(plan):
+    for packed, nseq, units in ((0, 1, 96), (0, 3, 32), (1, 32, 32), (1, 5, 400)):
+        assert plan(5000, nseq, units, packed, 1)[0] == 4096
