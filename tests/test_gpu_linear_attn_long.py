@@ -81,3 +81,20 @@ def compare(gdr, lens, Hk, Hv, dk, dv, dtype, seed, packed, decay):
 def test_one_long_sequence_among_many(gdr, lens, Hk, Hv, decay, dtype):
     """1024 workgroups and more of packed sequences, of which the forward cuts the long ones alone."""
     compare(gdr, lens, Hk, Hv, 64, 64, dtype, 900 + len(lens), True, decay)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("lens,Hk,Hv,dk,dv,packed,decay", [
+    ([4300] * 3, 16, 32, 64, 32, False, "layer"), ([4300] * 3, 32, 32, 64, 64, False, "head"), ([4097], 32, 96, 64, 32, False, "slow"),
+    ([4500] + [9] * 31, 16, 32, 64, 64, True, "layer"), ([0, 3] * 8 + [8300] + [9] * 20, 32, 32, 64, 96, True, "head"), ([5000], 8, 8, 128, 256, False, "layer")])
+def test_segments_of_4096_tokens(gdr, lens, Hk, Hv, dk, dv, packed, decay, dtype):
+    """So many heads that the backward is cut only where its sums would run over more than 4096 tokens, the last segment short
+    (of four tokens, of one), and a plain cut."""
+    compare(gdr, lens, Hk, Hv, dk, dv, dtype, 930 + len(lens) + dv, packed, decay)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("lens,Hk,Hv,dk,dv,packed,decay", [([6100], 40, 40, 64, 64, False, "layer"), ([3001, 17, 0, 2999], 20, 40, 64, 128, True, "head"),
+                                                           ([2500, 2500], 24, 24, 128, 96, False, "slow")])
+def test_segments_of_many_chunks(gdr, lens, Hk, Hv, dk, dv, packed, decay, dtype):
+    compare(gdr, lens, Hk, Hv, dk, dv, dtype, 960 + len(lens) + dv, packed, decay)
