@@ -196,10 +196,7 @@ gdr_status_t attn_sizes(const gdr_chunk_dims_t *dims, bool packed, AttnSizes *z)
     if (z->nq < 0 || z->nv < 0 || z->na < 0 || z->ns < 0 || z->nq > most || z->nv > most || z->ns > most ||
         prod({d.B, d.Hv, d.T, d.dk}) < 0 || prod({d.B, d.Hv, d.T, d.dk}) > most)
         return fail(GDR_ERR_DIMS, "sizes overflow");
-    // a launch holds, per (sequence or 256 tokens, value head), three roles' workgroups of at most four slices, and 8 more blocks
-    // of a state where those are joined; workgroups are numbered in 31 bits, eight heads of slack
-    const int64_t units = prod({z->nseq + prod({d.B, d.T / 256 + 1}) + 8, d.Hv, 32});
-    if (units < 0 || units > INT32_MAX) return fail(GDR_ERR_DIMS, "too many sequences or heads");
+    if (!gdr::attn_numbered(z->nseq, d.B, d.T, d.Hv)) return fail(GDR_ERR_DIMS, "too many sequences or heads");
     return GDR_OK;
 }
 

@@ -118,6 +118,16 @@ inline bool attn_together(int64_t dk, int64_t dv, int64_t segments, bool bf16) {
 // is no row (a negative number would be a bound without an end).
 constexpr int attn_extent(int n, int width, int first) { return n > 0 ? n * width - first : 0; }
 
+// Whether every launch's workgroups can be numbered in 31 bits. Per sequence and value head they are 32 at most: the blocks of a
+// 128 x 256 state where segments are joined; a step has 8, a sweep two roles of four column slices for twice the sequences (the last
+// segment of each is a part of one). Per token and value head they are an eighth at most: the sums of two value heads' gradients of 128
+// channels; a sweep has 8 in 4096 tokens, and with shorter segments some thousand in all. Sweeps round up to eight key heads.
+inline bool attn_numbered(int64_t nseq, int64_t B, int64_t T, int64_t Hv) {
+    if (nseq > INT32_MAX || B > INT32_MAX || T > INT32_MAX || Hv > INT32_MAX) return false;
+    const __int128 units = (__int128)nseq + (__int128)B * (T / 256 + 1) + 8;
+    return units * Hv * 32 <= INT32_MAX;
+}
+
 // The workspace's parts, in bytes from its beginning.
 struct AttnSpace {
     int64_t states, decays;                            // forward; the backward's first pair

@@ -3,6 +3,7 @@ are, and what is not worth a cut."""
 from __future__ import annotations
 
 import os
+import random
 import shutil
 import subprocess
 
@@ -52,3 +53,23 @@ def test_fewer_are_cut(plan, backward, units):
 def test_backward_segments_end_where_sums_cancel(plan):
     for packed, nseq, units in ((0, 1, 96), (0, 3, 32), (1, 32, 32), (1, 5, 400)):
         assert plan(5000, nseq, units, packed, 1)[0] == 4096
+
+
+def test_workgroups_are_numbered_in_31_bits(tmp_path):
+    """At the largest calls that are taken, and any others, no launch has 2^31 workgroups; a little larger ones are refused."""
+    exe = str(tmp_path / "driver")
+    subprocess.run([CXX, "-O1", "-std=c++17", "-Wall", os.path.join(HERE, "attn_launch_driver.cpp"), "-o", exe], check=True)
+    r, cases = random.Random(5), []
+    for _ in range(20000):
+        packed, group, dk, dv = r.randint(0, 1), r.choice([1, 2, 3, 8]), r.choice([64, 128]), 32 * r.randint(1, 8)
+        Hk = r.choice([1, 2, 5, 16, 64, 1000, 100000])
+        Hv, T = Hk * group, int(2 ** r.uniform(0, 31)) - 1
+        # sequences up to about what the rule leaves room for
+        room = max(1, (2 ** 26 // Hv - (T // 256 + 1 if packed else 0)) // (1 if packed else 1 + T // 256 + 1))
+        nseq = max(1, int(room * r.choice([1, 0.999, 0.5, 1e-3, 1e-6])))
+        cases.append((1 if packed else nseq, T, nseq, packed, Hk, Hv, dk, dv))
+    text = "\n".join(" ".join(map(str, c)) for c in cases)
+    out = [line.split() for line in subprocess.run([exe], input=text, capture_output=True, text=True, check=True).stdout.splitlines()]
+    taken = [int(most) for ok, most in out if ok == "1"]
+    assert len(out) == len(cases) and len(taken) > 2000 and max(taken) > 2 ** 30 and max(taken) < 2 ** 31 - 4096
+    assert any(ok == "0" for ok, _ in out)
