@@ -172,6 +172,16 @@ def _stream(t):
     return torch._C._cuda_getCurrentRawStream(t.device.index)  # current_stream(...).cuda_stream, without the object
 
 
+def _run(t, fn, *args):
+    """fn on t's device, which need not be the current one, and on the stream that is current there."""
+    if t.device.index != torch._C._cuda_getDevice():
+        with torch.cuda.device(t.device):
+            return _run(t, fn, *args)
+    status = fn(*args, _stream(t))
+    if status:
+        _check(status)
+
+
 def _need(t, name, dtype=None, shape=None, device=None):
     # what nearly every call brings, checked in one expression: a step's checks cost it more than its kernel
     if (device is not None and type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device
@@ -262,10 +272,10 @@ def chunk_fwd_bidir(q, k, v, log_alpha_fwd, beta_fwd, log_alpha_rev, beta_rev, h
     flags = (GDR_READ_PRE if read == "pre" else 0) | (GDR_ACCUMULATE if accumulate else 0) | \
         (GDR_QK_L2NORM if l2norm else 0)
     dims = ChunkDims(B, T, Hk, Hv, dk, dv, S if cu_seqlens is not None else 0, code, flags)
-    _check(lib().gdr_chunk_fwd_bidir(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha_fwd), _ptr(beta_fwd),
-                                     _ptr(log_alpha_rev), _ptr(beta_rev), _ptr(h0_fwd), _ptr(h0_rev),
-                                     _ptr(cu_seqlens), int(chunk), _ptr(out), _ptr(hT_f), _ptr(hT_r),
-                                     ctypes.byref(dims), _stream(q)))
+    _run(q, lib().gdr_chunk_fwd_bidir, _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha_fwd), _ptr(beta_fwd),
+         _ptr(log_alpha_rev), _ptr(beta_rev), _ptr(h0_fwd), _ptr(h0_rev),
+         _ptr(cu_seqlens), int(chunk), _ptr(out), _ptr(hT_f), _ptr(hT_r),
+         ctypes.byref(dims))
     return out, hT_f, hT_r
 
 
@@ -308,13 +318,13 @@ def _chunk(q, k, v, ga, gb, A_log, dt_bias, h0, cu_seqlens, chunk, read, reverse
         (GDR_ACCUMULATE if accumulate else 0) | (GDR_QK_L2NORM if l2norm else 0)
     dims = ChunkDims(B, T, Hk, Hv, dk, dv, S if cu_seqlens is not None else 0, code, flags)
     if gated:
-        _check(lib().gdr_chunk_fwd_gated(_ptr(q), _ptr(k), _ptr(v), _ptr(ga), _ptr(gb), _ptr(A_log),
-                                         _ptr(dt_bias), _ptr(h0), _ptr(cu_seqlens), int(chunk), _ptr(out),
-                                         _ptr(hT), ctypes.byref(dims), _stream(q)))
+        _run(q, lib().gdr_chunk_fwd_gated, _ptr(q), _ptr(k), _ptr(v), _ptr(ga), _ptr(gb), _ptr(A_log),
+             _ptr(dt_bias), _ptr(h0), _ptr(cu_seqlens), int(chunk), _ptr(out),
+             _ptr(hT), ctypes.byref(dims))
     else:
-        _check(lib().gdr_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(ga), _ptr(gb), _ptr(h0),
-                                   _ptr(cu_seqlens), int(chunk), _ptr(out), _ptr(hT),
-                                   ctypes.byref(dims), _stream(q)))
+        _run(q, lib().gdr_chunk_fwd, _ptr(q), _ptr(k), _ptr(v), _ptr(ga), _ptr(gb), _ptr(h0),
+             _ptr(cu_seqlens), int(chunk), _ptr(out), _ptr(hT),
+             ctypes.byref(dims))
     return out, hT
 
 
@@ -363,12 +373,12 @@ def _decode(q, k, v, ga, gb, A_log, dt_bias, state_in, state_out, out, read, l2n
     flags = (GDR_READ_PRE if read == "pre" else 0) | (GDR_QK_L2NORM if l2norm else 0)
     dims = DecodeDims(N, Hk, Hv, dk, dv, code, flags)
     if gated:
-        _check(lib().gdr_decode_step_gated(_ptr(q), _ptr(k), _ptr(v), _ptr(ga), _ptr(gb), _ptr(A_log),
-                                           _ptr(dt_bias), _ptr(state_in), _ptr(state_out), _ptr(out),
-                                           ctypes.byref(dims), _stream(q)))
+        _run(q, lib().gdr_decode_step_gated, _ptr(q), _ptr(k), _ptr(v), _ptr(ga), _ptr(gb), _ptr(A_log),
+             _ptr(dt_bias), _ptr(state_in), _ptr(state_out), _ptr(out),
+             ctypes.byref(dims))
     else:
-        _check(lib().gdr_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(ga), _ptr(gb), _ptr(state_in),
-                                     _ptr(state_out), _ptr(out), ctypes.byref(dims), _stream(q)))
+        _run(q, lib().gdr_decode_step, _ptr(q), _ptr(k), _ptr(v), _ptr(ga), _ptr(gb), _ptr(state_in),
+             _ptr(state_out), _ptr(out), ctypes.byref(dims))
     return out, state_out
 
 
@@ -411,9 +421,9 @@ def chunk_bwd(q, k, v, log_alpha, beta, dout, h0=None, cu_seqlens=None, dhT=None
     dv_ = torch.empty((B, Hv, T, dv), **f32)
     dla, dbe = torch.empty((B, Hv, T), **f32), torch.empty((B, Hv, T), **f32)
     dh0 = torch.empty((S, Hv, dk, dv), **f32) if want_dh0 else None
-    _check(lib().gdr_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(h0), _ptr(cu_seqlens),
-                               _ptr(dout), _ptr(dhT), _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(dla), _ptr(dbe), _ptr(dh0),
-                               _ptr(workspace), ctypes.c_int64(workspace.numel()), ctypes.byref(dims), _stream(q)))
+    _run(q, lib().gdr_chunk_bwd, _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(h0), _ptr(cu_seqlens),
+         _ptr(dout), _ptr(dhT), _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(dla), _ptr(dbe), _ptr(dh0),
+         _ptr(workspace), ctypes.c_int64(workspace.numel()), ctypes.byref(dims))
     return dq, dk_, dv_, dla, dbe, dh0
 
 
@@ -460,9 +470,9 @@ def delta_product_fwd(q, k, v, log_alpha, beta, h0=None, cu_seqlens=None, *, chu
     flags = (GDR_READ_PRE if read == "pre" else 0) | (GDR_ACCUMULATE if accumulate else 0) | \
         (GDR_QK_L2NORM if l2norm else 0)
     dims = ChunkDims(B, T, Hk, Hv, dk, dv, S if cu_seqlens is not None else 0, code, flags)
-    _check(lib().gdr_delta_product_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(h0),
-                                       _ptr(cu_seqlens), int(n), int(chunk), _ptr(out), _ptr(hT),
-                                       ctypes.byref(dims), _stream(q)))
+    _run(q, lib().gdr_delta_product_fwd, _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(h0),
+         _ptr(cu_seqlens), int(n), int(chunk), _ptr(out), _ptr(hT),
+         ctypes.byref(dims))
     return out, hT
 
 
@@ -517,9 +527,9 @@ def gdn2_chunk_fwd(q, k, v, g, b, w, h0=None, cu_seqlens=None, *, chunk: int = 6
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
         _need(workspace, "workspace", torch.uint8, None, dev)
         ws_ptr, ws_bytes = _ptr(workspace), workspace.numel()
-    _check(lib().gdr_gdn2_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(b), _ptr(w), _ptr(h0),
-                                    _ptr(cu_seqlens), int(chunk), _ptr(out), _ptr(hT), ws_ptr, ws_bytes,
-                                    ctypes.byref(dims), _stream(q)))
+    _run(q, lib().gdr_gdn2_chunk_fwd, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(b), _ptr(w), _ptr(h0),
+         _ptr(cu_seqlens), int(chunk), _ptr(out), _ptr(hT), ws_ptr, ws_bytes,
+         ctypes.byref(dims))
     return out, hT
 
 
@@ -573,10 +583,9 @@ def gdn2_chunk_fwd_bidir(q, k, v, fwd_gates, rev_gates, h0_fwd=None, h0_rev=None
         _need(workspace, "workspace", torch.uint8, None, dev)
         ws_ptr, ws_bytes = _ptr(workspace), workspace.numel()
     (gf, bf, wf), (gr, br, wr) = fwd_gates, rev_gates
-    _check(lib().gdr_gdn2_chunk_fwd_bidir(_ptr(q), _ptr(k), _ptr(v), _ptr(gf), _ptr(bf), _ptr(wf), _ptr(gr),
-                                          _ptr(br), _ptr(wr), _ptr(h0_fwd), _ptr(h0_rev), _ptr(cu_seqlens), int(chunk),
-                                          _ptr(out), _ptr(hT_f), _ptr(hT_r), ws_ptr, ws_bytes, ctypes.byref(dims),
-                                          _stream(q)))
+    _run(q, lib().gdr_gdn2_chunk_fwd_bidir, _ptr(q), _ptr(k), _ptr(v), _ptr(gf), _ptr(bf), _ptr(wf), _ptr(gr),
+         _ptr(br), _ptr(wr), _ptr(h0_fwd), _ptr(h0_rev), _ptr(cu_seqlens), int(chunk),
+         _ptr(out), _ptr(hT_f), _ptr(hT_r), ws_ptr, ws_bytes, ctypes.byref(dims))
     return out, hT_f, hT_r
 
 
@@ -605,9 +614,8 @@ def gdn2_chunk_fwd_noalloc(q, k, v, g, b, w, h0, cu_seqlens, out, hT, *, chunk: 
     flags = (GDR_READ_PRE if read == "pre" else 0) | (GDR_REVERSE if reverse else 0) | \
         (GDR_ACCUMULATE if accumulate else 0) | (GDR_QK_L2NORM if l2norm else 0)
     dims = ChunkDims(B, T, Hk, Hv, dk, dv, S if cu_seqlens is not None else 0, _dtype_code(dt), flags)
-    _check(lib().gdr_gdn2_chunk_fwd_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(b), _ptr(w), _ptr(h0),
-                                            _ptr(cu_seqlens), int(chunk), _ptr(out), _ptr(hT), ctypes.byref(dims),
-                                            _stream(q)))
+    _run(q, lib().gdr_gdn2_chunk_fwd_noalloc, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(b), _ptr(w), _ptr(h0),
+         _ptr(cu_seqlens), int(chunk), _ptr(out), _ptr(hT), ctypes.byref(dims))
     return out, hT
 
 
@@ -644,8 +652,8 @@ def gdn2_decode_step(q, k, v, g, b, w, state_in, state_out=None, out=None, *, re
         raise ValueError("read must be 'pre' or 'post'")
     flags = (GDR_READ_PRE if read == "pre" else 0) | (GDR_QK_L2NORM if l2norm else 0)
     dims = DecodeDims(N, Hk, Hv, dk, dv, code, flags)
-    _check(lib().gdr_gdn2_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(b), _ptr(w), _ptr(state_in),
-                                      _ptr(state_out), _ptr(out), ctypes.byref(dims), _stream(q)))
+    _run(q, lib().gdr_gdn2_decode_step, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(b), _ptr(w), _ptr(state_in),
+         _ptr(state_out), _ptr(out), ctypes.byref(dims))
     return out, state_out
 
 
@@ -706,9 +714,9 @@ def channel_scan_fwd(x, a, b, A_log, dt_bias, h0=None, cu_seqlens=None, *, rever
             raise GdrError(2, lib().gdr_last_error().decode())
         states = torch.empty(n, dtype=torch.float32, device=dev)
     ws = _workspace(workspace, lib().gdr_channel_scan_fwd_workspace_bytes(d, packed), dev)
-    _check(lib().gdr_channel_scan_fwd(_ptr(x), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias), _ptr(h0),
-                                      _ptr(cu_seqlens), _ptr(out), _ptr(hT), _ptr(states), _ptr(ws),
-                                      0 if ws is None else ws.numel(), d, _stream(x)))
+    _run(x, lib().gdr_channel_scan_fwd, _ptr(x), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias), _ptr(h0),
+         _ptr(cu_seqlens), _ptr(out), _ptr(hT), _ptr(states), _ptr(ws),
+         0 if ws is None else ws.numel(), d)
     return out, hT, states
 
 
@@ -728,10 +736,10 @@ def channel_scan_bwd(x, a, b, A_log, dt_bias, states, dout, cu_seqlens=None, dhT
     dA_log, ddt_bias = torch.empty_like(A_log), torch.empty_like(A_log)
     dh0 = torch.empty((S, dims.D), dtype=torch.float32, device=dev) if want_dh0 else None
     ws = _workspace(workspace, lib().gdr_channel_scan_bwd_workspace_bytes(d, packed), dev)
-    _check(lib().gdr_channel_scan_bwd(_ptr(x), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias), _ptr(states),
-                                      _ptr(cu_seqlens), _ptr(dout), _ptr(dhT), _ptr(dx), _ptr(da), _ptr(db),
-                                      _ptr(dA_log), _ptr(ddt_bias), _ptr(dh0), _ptr(ws),
-                                      0 if ws is None else ws.numel(), d, _stream(x)))
+    _run(x, lib().gdr_channel_scan_bwd, _ptr(x), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias), _ptr(states),
+         _ptr(cu_seqlens), _ptr(dout), _ptr(dhT), _ptr(dx), _ptr(da), _ptr(db),
+         _ptr(dA_log), _ptr(ddt_bias), _ptr(dh0), _ptr(ws),
+         0 if ws is None else ws.numel(), d)
     return dx, da, db, dA_log, ddt_bias, dh0
 
 
@@ -759,8 +767,8 @@ def channel_scan_step(x, a, b, A_log, dt_bias, state_in, state_out=None, out=Non
     else:
         _need(out, "out", dt, (N, D), dev)
     dims = ScanDims(N, 1, D, 0, code, 0)
-    _check(lib().gdr_channel_scan_step(_ptr(x), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias), _ptr(state_in),
-                                       _ptr(state_out), _ptr(out), ctypes.byref(dims), _stream(x)))
+    _run(x, lib().gdr_channel_scan_step, _ptr(x), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias), _ptr(state_in),
+         _ptr(state_out), _ptr(out), ctypes.byref(dims))
     return out, state_out
 
 
@@ -812,8 +820,8 @@ def gated_ffn_fwd(x, w_gate, w_up, *, act: str = "silu", out=None, want_saved: b
         _need(out, "out", x.dtype, shape, dev)
     gate = torch.empty(shape, dtype=saved_dtype, device=dev) if want_saved else None
     up = torch.empty_like(gate) if want_saved else None
-    _check(lib().gdr_gated_ffn_fwd(_ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(out), _ptr(gate), _ptr(up),
-                                   ctypes.byref(dims), _stream(x)))
+    _run(x, lib().gdr_gated_ffn_fwd, _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(out), _ptr(gate), _ptr(up),
+         ctypes.byref(dims))
     return out, gate, up
 
 
@@ -828,9 +836,9 @@ def gated_ffn_bwd(x, w_gate, w_up, gate, up, dh, *, act: str = "silu", workspace
     _need(dh, "dh", x.dtype, shape, dev)
     dx, dwg, dwu = torch.empty_like(x), torch.empty_like(w_gate), torch.empty_like(w_up)
     ws = _workspace(workspace, lib().gdr_gated_ffn_bwd_workspace_bytes(ctypes.byref(dims)), dev)
-    _check(lib().gdr_gated_ffn_bwd(_ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(gate), _ptr(up), _ptr(dh), _ptr(dx),
-                                   _ptr(dwg), _ptr(dwu), _ptr(ws), 0 if ws is None else ws.numel(),
-                                   ctypes.byref(dims), _stream(x)))
+    _run(x, lib().gdr_gated_ffn_bwd, _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(gate), _ptr(up), _ptr(dh), _ptr(dx),
+         _ptr(dwg), _ptr(dwu), _ptr(ws), 0 if ws is None else ws.numel(),
+         ctypes.byref(dims))
     return dx, dwg, dwu
 
 
@@ -857,8 +865,8 @@ def linear_ce_fwd(x, weight, targets, *, workspace=None):
     loss = torch.empty(dims.N, dtype=torch.float32, device=dev)
     lse = torch.empty_like(loss)
     ws = _workspace(workspace, lib().gdr_linear_ce_fwd_workspace_bytes(ctypes.byref(dims)), dev)
-    _check(lib().gdr_linear_ce_fwd(_ptr(x), _ptr(weight), _ptr(targets), _ptr(loss), _ptr(lse), _ptr(ws),
-                                   0 if ws is None else ws.numel(), ctypes.byref(dims), _stream(x)))
+    _run(x, lib().gdr_linear_ce_fwd, _ptr(x), _ptr(weight), _ptr(targets), _ptr(loss), _ptr(lse), _ptr(ws),
+         0 if ws is None else ws.numel(), ctypes.byref(dims))
     return loss, lse
 
 
@@ -870,8 +878,8 @@ def linear_ce_bwd(x, weight, targets, lse, dloss, *, workspace=None):
     _need(dloss, "dloss", torch.float32, (dims.N,), dev)
     dx, dw = torch.empty_like(x), torch.empty_like(weight)
     ws = _workspace(workspace, lib().gdr_linear_ce_bwd_workspace_bytes(ctypes.byref(dims)), dev)
-    _check(lib().gdr_linear_ce_bwd(_ptr(x), _ptr(weight), _ptr(targets), _ptr(lse), _ptr(dloss), _ptr(dx), _ptr(dw),
-                                   _ptr(ws), 0 if ws is None else ws.numel(), ctypes.byref(dims), _stream(x)))
+    _run(x, lib().gdr_linear_ce_bwd, _ptr(x), _ptr(weight), _ptr(targets), _ptr(lse), _ptr(dloss), _ptr(dx), _ptr(dw),
+         _ptr(ws), 0 if ws is None else ws.numel(), ctypes.byref(dims))
     return dx, dw
 
 
@@ -922,8 +930,8 @@ def linear_attn_fwd(q, k, v, log_alpha, h0=None, cu_seqlens=None, *, out=None, h
         hT = torch.empty(state, dtype=torch.float32, device=dev)
     d = ctypes.byref(dims)
     ws = _workspace(workspace, lib().gdr_linear_attn_fwd_workspace_bytes(d, int(cu_seqlens is not None)), dev)
-    _check(lib().gdr_linear_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(h0), _ptr(cu_seqlens), _ptr(out),
-                                     _ptr(hT), _ptr(ws), 0 if ws is None else ws.numel(), d, _stream(q)))
+    _run(q, lib().gdr_linear_attn_fwd, _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(h0), _ptr(cu_seqlens), _ptr(out),
+         _ptr(hT), _ptr(ws), 0 if ws is None else ws.numel(), d)
     return out, hT
 
 
@@ -941,9 +949,9 @@ def linear_attn_bwd(q, k, v, log_alpha, dout, h0=None, cu_seqlens=None, dhT=None
     dh0 = torch.empty(state, dtype=torch.float32, device=dev) if want_dh0 else None
     d = ctypes.byref(dims)
     ws = _workspace(workspace, lib().gdr_linear_attn_bwd_workspace_bytes(d, int(cu_seqlens is not None)), dev)
-    _check(lib().gdr_linear_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(h0), _ptr(cu_seqlens), _ptr(dout),
-                                     _ptr(dhT), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dla), _ptr(dh0), _ptr(ws),
-                                     0 if ws is None else ws.numel(), d, _stream(q)))
+    _run(q, lib().gdr_linear_attn_bwd, _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(h0), _ptr(cu_seqlens), _ptr(dout),
+         _ptr(dhT), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dla), _ptr(dh0), _ptr(ws),
+         0 if ws is None else ws.numel(), d)
     return dq, dk, dv, dla, dh0
 
 
@@ -976,8 +984,8 @@ def linear_attn_step(q, k, v, log_alpha, state_in, state_out=None, out=None):
     else:
         _need(out, "out", dt, (N, Hv, dv), dev)
     dims = DecodeDims(N, Hk, Hv, dk, dv, code, GDR_HEAD_DECAY if head else 0)
-    _check(lib().gdr_linear_attn_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(state_in), _ptr(state_out),
-                                      _ptr(out), ctypes.byref(dims), _stream(q)))
+    _run(q, lib().gdr_linear_attn_step, _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(state_in), _ptr(state_out),
+         _ptr(out), ctypes.byref(dims))
     return out, state_out
 
 
@@ -1065,8 +1073,8 @@ def qk_norm_rope_fwd(q, k, w_q, w_k, inv_freq, positions=None, *, eps: float = 1
         out_k = k.new_empty(like_k)
     else:
         _need(out_k, "out_k", q.dtype, like_k, dev)
-    _check(lib().gdr_qk_norm_rope_fwd(_ptr(q), _ptr(k), _ptr(w_q), _ptr(w_k), _ptr(inv_freq), _ptr(positions), _ptr(out_q),
-                                      _ptr(out_k), ctypes.byref(dims), _stream(q)))
+    _run(q, lib().gdr_qk_norm_rope_fwd, _ptr(q), _ptr(k), _ptr(w_q), _ptr(w_k), _ptr(inv_freq), _ptr(positions), _ptr(out_q),
+         _ptr(out_k), ctypes.byref(dims))
     return out_q, out_k
 
 
@@ -1096,9 +1104,9 @@ def qk_norm_rope_bwd(q, k, w_q, w_k, inv_freq, doq, dok, positions=None, *, eps:
     dw_k = None if w_k is None else torch.empty_like(w_k)
     need = lib().gdr_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(dims)) if dw_q is not None or dw_k is not None else 0
     ws = _workspace(workspace, need, dev)
-    _check(lib().gdr_qk_norm_rope_bwd(_ptr(q), _ptr(k), _ptr(w_q), _ptr(w_k), _ptr(inv_freq), _ptr(positions), _ptr(doq), _ptr(dok),
-                                      _ptr(dq), _ptr(dk), _ptr(dw_q), _ptr(dw_k), _ptr(ws), 0 if ws is None else ws.numel(),
-                                      ctypes.byref(dims), _stream(q)))
+    _run(q, lib().gdr_qk_norm_rope_bwd, _ptr(q), _ptr(k), _ptr(w_q), _ptr(w_k), _ptr(inv_freq), _ptr(positions), _ptr(doq), _ptr(dok),
+         _ptr(dq), _ptr(dk), _ptr(dw_q), _ptr(dw_k), _ptr(ws), 0 if ws is None else ws.numel(),
+         ctypes.byref(dims))
     return dq, dk, dw_q, dw_k
 
 
@@ -1108,5 +1116,5 @@ def selftest_mfma(a, b):
     _need(a, "a", torch.float32, (16, 32))
     _need(b, "b", torch.float32, (32, 16), a.device)
     d = torch.empty((3, 16, 16), dtype=torch.float32, device=a.device)
-    _check(lib().gdr_selftest_mfma(_ptr(a), _ptr(b), _ptr(d), _stream(a)))
+    _run(a, lib().gdr_selftest_mfma, _ptr(a), _ptr(b), _ptr(d))
     return d

@@ -15,9 +15,10 @@
  *   - Every tensor pointer is a DEVICE pointer to contiguous row-major memory, 16-byte
  *     aligned; the `dims` structs are HOST pointers. The caller owns all memory: the
  *     library allocates nothing on the device and keeps no state between calls.
- *   - Work is enqueued on `stream` (a hipStream_t; NULL is the null stream) and the call
- *     returns without synchronising. No host read of device data happens, so calls can
- *     be captured into a HIP graph.
+ *   - Work is enqueued on `stream` (a hipStream_t; NULL is the null stream) of the current HIP
+ *     device, which must own the stream and the memory, and the call returns without
+ *     synchronising. No host read of device data happens, so calls can be captured into a
+ *     HIP graph.
  *   - Arguments are validated on the host before anything is launched. A non-GDR_OK
  *     status means nothing was enqueued; gdr_last_error() then names the offending
  *     argument (thread-local text, valid until the next call on that thread).
