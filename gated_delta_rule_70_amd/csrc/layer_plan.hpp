@@ -105,14 +105,11 @@ inline int attn_tiles(int64_t db, int64_t workgroups = INT64_MAX) { return db <=
 inline int64_t attn_slices(int64_t db, int tiles) { return (db + 64 * tiles - 1) / (64 * tiles); }
 inline int64_t attn_slices(int64_t db) { return attn_slices(db, attn_tiles(db)); }
 
-// Whether the backward's gradients of q, k and v are one launch, where the same kernel takes keys' and values' sizes. `segments`: of all
-// value heads. bf16: up to 1024 workgroups, since v's gradient then goes through three parts to an operand and rows' products as
-// well. A backward of 77 tokens of 16 heads of 128 takes 27 us so, 39 in two launches (256 tokens: 40 and 60; four value heads to
-// a key head: 49 and 69), 8 heads of 2048 tokens 85 and 91 (768 workgroups), 32 heads of 32,768 tokens 1275 and 1231. fp32, which
-// has one form: 32 and 48, 64 and 99, 107 and 113, 2842 and 2903.
-inline bool attn_together(int64_t dk, int64_t dv, int64_t segments, bool bf16) {
-    return dv <= 128 && (dv <= 64) == (dk <= 64) && (!bf16 || 3 * segments <= 4 * kComputeUnits);
-}
+// Whether the backward's gradients of q, k and v are one launch: where the same kernel takes keys' and values' sizes. A backward of 77
+// tokens of 16 heads of 128 takes 28 us so, 43 in two launches (256 tokens: 42 and 65; four value heads to a key head: 38 and 52),
+// 16 x 512 tokens 160 and 165, 64 x 512 561 and 585, 4 x 4096 353 and 372, 32 heads of 32,768 tokens 1293 and 1329; fp32 34 and 51, 66 and 101,
+// 312 and 325, 1149 and 1205, 765 and 791, 2906 and 2969.
+inline bool attn_together(int64_t dk, int64_t dv) { return dv <= 128 && (dv <= 64) == (dk <= 64); }
 
 // Elements that a chunk's n rows of `width` span from column `first` on: what a workgroup may touch from there. None where there
 // is no row (a negative number would be a bound without an end).

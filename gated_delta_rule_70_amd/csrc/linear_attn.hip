@@ -1147,7 +1147,7 @@ hipError_t bwd(const AttnCall &c, hipStream_t s) {
     v.in_slots = k.in_slots;
     v.s_in = k.s_in;
     v.s_out = p.seg ? nullptr : c.dh0;
-    if (attn_together(dk, dv, p.slots * c.Hv, is_bf16<E>())) {
+    if (attn_together(dk, dv)) {
         v.other = c.dout;  // read and multiplied with as the other roles' are; the products go nowhere
         q.shares = k.shares = group > 1;
         if constexpr (is_bf16<E>()) {
