@@ -725,8 +725,8 @@ __device__ __forceinline__ double sum_all(double v, double *held) {
     return held[0] + held[1] + held[2] + held[3];
 }
 
-// Four elements of one head's state a thread: each segment's own state is replaced by the one that enters it, or, with `cuts` (whose
-// first one of a sequence names the workgroup), that of the segment before each cut by the one that goes over it. States are
+// Four elements of one head's state a thread: each segment's own state is replaced by the one that enters it, or, with `cuts` (packed, the first
+// one of a sequence names the workgroup), that of the segment before each cut by the one that goes over it. States are
 // [rows][cols] here, init and last the same or, turned, [cols][rows]. With `ends` (backwards, behind the forward's states), each
 // workgroup leaves its part of <the adjoint that enters segment i from behind, the state there>, which enters segment i + 1.
 struct Join {
@@ -743,11 +743,11 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Join j) {
     const int64_t elems = (int64_t)j.rows * j.cols;
     const unsigned blocks = (unsigned)(elems / 1024), id = (unsigned)block_id(), unit = id / blocks, block = id % blocks;
     const unsigned which = unit / (unsigned)a.Hv, head = unit % (unsigned)a.Hv;
-    if (which >= (j.cuts ? a.cuts : a.nseq)) return;
+    if (which >= (j.cuts && a.cu ? a.cuts : a.nseq)) return;
     const int64_t e = block * 1024 + threadIdx.x * 4;
     unsigned seq = which;
-    int first = (int)(which * a.per_seq), n = (int)a.per_seq;
-    if (j.cuts) {
+    int n = (int)a.per_seq - (j.cuts ? 1 : 0), first = (int)which * n;
+    if (j.cuts && a.cu) {
         const Span sp = span_of(a, which, true);
         if (!sp.some || !sp.first()) return;
         seq = (unsigned)sp.seq;
@@ -1043,7 +1043,7 @@ hipError_t sweep(AttnArgs a, int first, int n, hipStream_t s) {
 }
 
 hipError_t join(const AttnArgs &a, const Join &j, hipStream_t s) {
-    hipLaunchKernelGGL(join_kernel, grid_of((j.cuts ? a.cuts : a.nseq) * a.Hv * (j.rows * j.cols / 1024), 256), dim3(256), 0, s, a, j);
+    hipLaunchKernelGGL(join_kernel, grid_of((j.cuts && a.cu ? a.cuts : a.nseq) * a.Hv * (j.rows * j.cols / 1024), 256), dim3(256), 0, s, a, j);
     return hipGetLastError();
 }
 
