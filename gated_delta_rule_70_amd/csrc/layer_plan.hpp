@@ -59,18 +59,22 @@ struct AttnPlan {
     int64_t seg, per_seq, slots;
 };
 // `units`: workgroups of a whole sequence (heads and column slices). Split, into about 512 of whole chunks, where whole sequences
-// leave too many compute units idle to be worth less than the states' sweep and the second read: fewer than 192 of them, 96 in the
-// backward, which has each twice. Sequences of 4096 tokens of 16 heads of 128, bf16, split and whole: forward 8 of them (128) 239 and 289 us, 12 (192)
-// 404 and 385, 18 570 and 499, 23 894 and 531; backward 4 (64) 382 and 479, 6 (96) 640 and 577, 10 990 and 670; of 1024 tokens
-// forward 8 89 and 86, backward 4 149 and 132; forward fp32 4 316 and 497, 8 527 and 504. Up to 256 tokens one workgroup's few chunks take less
-// than the two launches that a split adds, or as long: 192 tokens of 16 heads 20 us whole and 23 split, 256 24 and 23, 320 28
-// and 24, backward 49 and 44. The backward's segments end at 4096 tokens, since sums over them cancel. Packed, fewer than
-// 1024 workgroups are split, since their lengths differ and are not known here.
+// leave too many compute units idle to be worth less than the states' sweep and the second read: fewer than 192 of them, 96 in
+// the backward, which has each twice. Sequences of 4096 tokens of 16 heads of 128, bf16, split and whole: forward 8 of them (128)
+// 239 and 289 us, 12 (192) 404 and 385, 18 570 and 499, 23 894 and 531; backward 4 (64) 382 and 479, 6 (96) 640 and 577, 10 990
+// and 670; of 1024 tokens forward 8 89 and 86, backward 4 149 and 132; forward fp32 4 316 and 497, 8 527 and 504. Values of 256
+// channels, whose gradients of q and k have one workgroup a compute unit: 6 1051 and 1168, 8 1345 and 1187. 512 workgroups: 4
+// sequences forward in segments of 512 tokens take 125 us, of 256 154, of 1024 146 (backward 351, 425 and 366); 2048 tokens of 16
+// heads would take 42 in 128 or 256, 51 in the 64 that this gives. Up to 256 tokens one workgroup's few chunks take less than the
+// two launches that a split adds, or as long: 192 tokens of 16 heads 20 us whole and 23 split, 256 24 and 23, 320 28 and 24,
+// backward 49 and 44. The backward's segments end at 4096 tokens, since sums over them cancel. Packed, fewer than 1024 workgroups
+// are split, since their lengths differ and are not known here.
 //
 // Packed sequences of 1024 workgroups and more: the forward cuts only those that are longer than their heads' share of the card,
-// for two launches that find nothing to do otherwise. 16 heads of 128: a document of 100,000 tokens among 63 of 500 takes 913 us so, 9289 whole; 3000
-// among 63 of 40 86 us and 298; 64 of 100 tokens 83 and 68, 64 of 512 198 and 210. Not below 2048 tokens, nor where sequences
-// are shorter than a chunk in the mean, since the workspace has a state for each of them. The backward's states are of all segments.
+// for two launches that find nothing to do otherwise. 16 heads of 128: a document of 100,000 tokens among 63 of 500 takes 913 us
+// so, 9289 whole; 3000 among 63 of 40 86 us and 298; 64 of 100 tokens 83 and 68, 64 of 512 198 and 210. Not below 2048 tokens,
+// nor where sequences are shorter than a chunk in the mean, since the workspace has a state for each of them. The backward's
+// states are of all segments.
 inline AttnPlan attn_plan(int64_t T, int64_t nseq, int64_t units, bool packed, bool backward) {
     AttnPlan p{0, 1, nseq};
     const int64_t rows = packed ? T : nseq * T;
@@ -99,16 +103,16 @@ struct Divisor {
 
 // Columns of a workgroup of 4 waves: a wave takes 16 or 32 (every column slice forms the scores again). 16 also where the slices
 // may be narrower and no more than 256 workgroups come of 32, so that the chip holds two of the others side by side: 77 tokens of
-// 16 heads of 128 take 13.3 us so, 17.1 with 32 (fp32 16.4 and 24.5), 256 tokens 21.6 and 27.8 (fp32 35.4 and 55.3). With up to
-// 512 workgroups 8192 tokens take 96 us so, 83 with 32.
+// 16 heads of 128 take 15.2 us so, 19.6 with 32 (fp32 17.9 and 25.9), 256 tokens 24.4 and 31.6 (fp32 37.1 and 56.6). With up to
+// 512 workgroups 8192 tokens take 98 us so, 84 with 32.
 inline int attn_tiles(int64_t db, int64_t workgroups = INT64_MAX) { return db <= 64 || workgroups <= kComputeUnits ? 1 : 2; }
 inline int64_t attn_slices(int64_t db, int tiles) { return (db + 64 * tiles - 1) / (64 * tiles); }
 inline int64_t attn_slices(int64_t db) { return attn_slices(db, attn_tiles(db)); }
 
-// Whether the backward's gradients of q, k and v are one launch: where the same kernel takes keys' and values' sizes. A backward of 77
-// tokens of 16 heads of 128 takes 28 us so, 43 in two launches (256 tokens: 42 and 65; four value heads to a key head: 38 and 52),
-// 16 x 512 tokens 160 and 165, 64 x 512 561 and 585, 4 x 4096 353 and 372, 32 heads of 32,768 tokens 1293 and 1329; fp32 34 and 51, 66 and 101,
-// 312 and 325, 1149 and 1205, 765 and 791, 2906 and 2969.
+// Whether the backward's gradients of q, k and v are one launch: where the same kernel takes keys' and values' sizes. A backward
+// of 77 tokens of 16 heads of 128 takes 28 us so, 43 in two launches (256 tokens: 42 and 65; four value heads to a key head: 38
+// and 52), 16 x 512 tokens 160 and 165, 64 x 512 561 and 585, 4 x 4096 353 and 372, 32 heads of 32,768 tokens 1293 and 1329; fp32
+// 34 and 51, 66 and 101, 312 and 325, 1149 and 1205, 765 and 791, 2906 and 2969.
 inline bool attn_together(int64_t dk, int64_t dv) { return dv <= 128 && (dv <= 64) == (dk <= 64); }
 
 // Elements that a chunk's n rows of `width` span from column `first` on: what a workgroup may touch from there. None where there

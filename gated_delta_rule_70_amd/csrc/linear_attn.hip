@@ -15,17 +15,21 @@
 // with the sum taken to the end of t's segment.
 //
 // Rounding. q, k, v and dout are matrix operands as they are. What is formed from them and is an operand in turn (the state, the
-// scores, the decayed rows) enters as a sum of three bf16 numbers, which is off by 2^-25 of it at most: results whose terms cancel
-// are those of fp32 products. Two numbers (2^-17) in the forward and dv took 434 us for 131,072 tokens of 8 heads where three take 474, and 482
-// for 501 in training 4 x 4096 tokens of 16 heads.
+// scores, the decayed rows) enters as a sum of three bf16 numbers, which is off by 2^-25 of it at most: results whose terms
+// cancel are those of fp32 products. Two (2^-17) in the forward and dv took 434 us for 131,072 tokens of 8 heads where three take
+// 474, and 490 for 498 in training 4 x 4096 tokens of 16 heads.
 //
-// What bounds it. A chunk of 64 tokens of a 128 x 128 head is 48 KB in, 16 KB out and 6.3 MFLOP (10.5 as executed, in parts). A
-// workgroup of four waves takes 14,600 cycles a chunk with a second one beside it on the compute unit, 12,000 alone (scores 3000,
-// H^T x 2900, scores times z 1700, the state 3100, copies 1100); the matrix instructions are 2600 of them, the other vector
-// instructions 2800. Without any of the products the same copies and barriers take 52 us a sweep of 4 x 4096 tokens of 16 heads
-// (5.8 TB/s), with them 77 to 90, the lower where the card holds 2.4 GHz, the higher at the 2.1 GHz it falls to under this load.
-// So the long sweeps are bound by memory and power together. Eight waves a workgroup (one on a compute unit) took 103 us,
-// two such workgroups 113 (registers: 128 a thread spill).
+// What bounds it. A chunk of 64 tokens of a 128 x 128 head is 48 KB in, 16 KB out and 6.3 MFLOP, 15 as executed (in parts). Two
+// workgroups of four waves share a compute unit; eight chunks of a forward sweep of 4 x 4096 tokens of 16 heads take the 512 of
+// them 170,000 cycles (88 to 101 us), of which the matrix cores are busy 35% and LDS 44%, and the waves wait 34% for memory, LDS
+// and barriers and 34% to issue. Without any of the products the same copies and barriers take 52 us (5.8 TB/s). So the long
+// sweeps are bound by the order copies, scores, products, state in two waves a SIMD. Eight waves a workgroup (one on a compute
+// unit) were slower by a tenth or more, two such workgroups too (registers: 128 a thread spill). The gradients' sweep of 128
+// columns takes all 256 registers of its two waves a SIMD and spills 3 to 7 of them (16 to 32 bytes a lane; the next chunk's rows
+// and the rows of the products are held over the chunk). That of values of more than 128 channels (x and y are values there)
+// leaves one workgroup a compute unit, 106 of its accumulators in AGPRs: the backward of 4 x 4096 tokens of 16 heads takes 668 us
+// for values of 160 channels, which are multiplied as 256, 778
+// for 256, 383 for 128 (forward 204, 244 and 153).
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -126,7 +130,7 @@ __device__ __forceinline__ Rows rows_at(const void *p, int bytes) {
 }
 constexpr int kNowhere = 0x40000000;  // an offset past every chunk
 // Results are stored past the caches' keeping, which leaves them to k and v, read again by the next launch: 4 x 4096 tokens of 16
-// heads train in 499 us so, 512 without; 131,072 tokens forward take 432 us, 426 without.
+// heads train in 471 us so, 474 without; 131,072 tokens forward take 458 us either way.
 constexpr int kPast = 2;
 // N elements of a row from a byte offset on
 template <typename E, int N>
@@ -554,7 +558,8 @@ __global__ __launch_bounds__(NW * 64, DA > 128 ? 1 : NW / 2) void sweep_kernel(A
                     if (wave + q * NW < kTiles) *reinterpret_cast<floatx4 *>(p) = s[q];
                 }
             }
-            // e^c H^T x. Products go before the other workgroup's copies and scores: training 509 us so, 520 without.
+            // e^c H^T x. Products go before the other workgroup's copies and scores: training 471 us so, 479
+            // without, 131,072 tokens forward 458 and 471.
             __builtin_amdgcn_s_setprio(1);
             floatx4 o[TI][NT];
 #pragma unroll
@@ -725,10 +730,11 @@ __device__ __forceinline__ double sum_all(double v, double *held) {
     return held[0] + held[1] + held[2] + held[3];
 }
 
-// Four elements of one head's state a thread: each segment's own state is replaced by the one that enters it, or, with `cuts` (packed, the first
-// one of a sequence names the workgroup), that of the segment before each cut by the one that goes over it. States are
-// [rows][cols] here, init and last the same or, turned, [cols][rows]. With `ends` (backwards, behind the forward's states), each
-// workgroup leaves its part of <the adjoint that enters segment i from behind, the state there>, which enters segment i + 1.
+// Four elements of one head's state a thread: each segment's own state is replaced by the one that enters it, or, with `cuts`
+// (packed, the first one of a sequence names the workgroup), that of the segment before each cut by the one that goes over it.
+// States are [rows][cols] here, init and last the same or, turned, [cols][rows]. With `ends` (backwards, behind the forward's
+// states), each workgroup leaves its part of <the adjoint that enters segment i from behind, the state there>, which enters
+// segment i + 1.
 struct Join {
     float *states;
     const float *decays, *init;

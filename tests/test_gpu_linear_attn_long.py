@@ -98,3 +98,32 @@ def test_segments_of_4096_tokens(gdr, lens, Hk, Hv, dk, dv, packed, decay, dtype
                                                            ([2500, 2500], 24, 24, 128, 96, False, "slow")])
 def test_segments_of_many_chunks(gdr, lens, Hk, Hv, dk, dv, packed, decay, dtype):
     compare(gdr, lens, Hk, Hv, dk, dv, dtype, 960 + len(lens) + dv, packed, decay)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_other_boundaries_in_one_graph(gdr, dtype):
+    """A captured forward and backward, replayed with other packed boundaries of as many tokens: one long document here, another
+    there, none at all, empty sequences; every replay has the eager calls' bits."""
+    H, S = 16, 64
+    lens = [[40] * 30 + [3000] + [40] * 33, [3000] + [40] * 63, [86] * 48 + [87] * 16, [0] * 50 + [2000, 0, 17, 3503] + [0] * 10]
+    T = sum(lens[0])
+    assert all(sum(x) == T and len(x) == S for x in lens)
+    say("boundaries in a graph %s" % dtype)
+    case = attn_case(lens[0], H, H, 64, 64, dtype, 990, True)
+    dout, dhT = cuda(upstream(case, 991))
+    q, k, v, la, h, cu = cuda(case)
+    bounds = [torch.tensor([0] + x).cumsum(0).to(torch.int32).cuda() for x in lens]
+    both = lambda: (*gdr.linear_attn_fwd(q, k, v, la, h, cu), *gdr.linear_attn_bwd(q, k, v, la, dout, h, cu, dhT))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = both()
+    for i in (1, 2, 3, 0, 2, 1):
+        cu.copy_(bounds[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, both())), i
