@@ -21,7 +21,7 @@
 //
 // What bounds it. A chunk of 64 tokens of a 128 x 128 head is 48 KB in, 16 KB out and 6.3 MFLOP, 15 as executed (in parts). Two
 // workgroups of four waves share a compute unit; eight chunks of a forward sweep of 4 x 4096 tokens of 16 heads take the 512 of
-// them 170,000 cycles (88 to 101 us), of which the matrix cores are busy 35% and LDS 44%, and the waves wait 34% for memory, LDS
+// them 170,000 cycles (88 to 101 us), of which the matrix cores are busy 35% and LDS 45%, and the waves wait 34% for memory, LDS
 // and barriers and 34% to issue. Without any of the products the same copies and barriers take 52 us (5.8 TB/s). So the long
 // sweeps are bound by the order copies, scores, products, state in two waves a SIMD. Eight waves a workgroup (one on a compute
 // unit) were slower by a tenth or more, two such workgroups too (registers: 128 a thread spill). The gradients' sweep of 128

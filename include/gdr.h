@@ -709,7 +709,8 @@ typedef struct gdr_qk_dims {
  *   workspace    at least gdr_qk_norm_rope_bwd_workspace_bytes(dims) bytes; not needed (NULL) without dw_q and dw_k
  *
  * Sums are held in fp32, the weights' gradients over many tokens in fp64; of bf16 tensors only the results are
- * rounded to bf16, once. Squares of x must not overflow fp32. Errors: as gdr_channel_scan_fwd, and
+ * rounded to bf16, once. Squares of x must not overflow fp32, nor, with eps 0,
+ * vanish in it. Errors: as gdr_channel_scan_fwd, and
  * GDR_ERR_UNSUPPORTED for d and rot.
  */
 int64_t gdr_qk_norm_rope_bwd_workspace_bytes(const gdr_qk_dims_t *dims);
