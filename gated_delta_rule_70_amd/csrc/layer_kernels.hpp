@@ -65,12 +65,12 @@ struct AttnRole {
     const void *other;   // like out: each row's product with out's goes to dot, [B][Hv][T], if that is wanted
     float *dot;
     const float *s_in;   // entering states by slot (in_slots) or sequence, or null for zeros
-    const float *s_cuts;  // with cuts: the states that go over them, turned (s_in is for the sequences' first segments)
-    float *s_out;        // states that sequences end with; without outputs, the segments' own, by slot (cut)
-    float *decay;        // without outputs: the segments' decays [slots (cuts)][Hv]
+    const float *s_cuts; // with cuts: entering states of the segments of cut sequences, by slot and turned (s_in is for the others)
+    float *s_out;        // states that sequences end with; without outputs, the segments' own, by slot
+    float *decay;        // without outputs: the segments' decays [slots][Hv]
     int32_t da, db;
     bool xk, yk, zk, ok, reverse, in_turned, out_turned, in_slots;  // *_turned: the state is stored as [db][da]
-    bool cuts;           // forwards: states between segments lie by cut, and only the segments before one have a state of their own
+    bool cuts;           // forwards: only segments that another one follows have a state of their own
     bool shares;         // mixed form: out is fp32
 };
 

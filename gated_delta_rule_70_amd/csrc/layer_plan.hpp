@@ -54,7 +54,7 @@ constexpr int kAttnChunk = 64;  // tokens of a bf16 chunk; fp32 chunks are half 
 
 // How a call walks the sequences: whole (seg 0), or in segments that are walked side by side once a pass has left each
 // one's own state. Packed segments of sequence s begin at slot cu[s] / seg + s; where one is followed by another, a sequence has a
-// cut, and the forward keeps states at those alone.
+// cut, and the forward forms states of the segments before those alone.
 struct AttnPlan {
     int64_t seg, per_seq, slots;
 };
@@ -72,7 +72,7 @@ struct AttnPlan {
 //
 // Packed sequences of 1024 workgroups and more: the forward cuts only those that are longer than their heads' share of the card,
 // for two launches that find nothing to do otherwise. 16 heads of 128: a document of 100,000 tokens among 63 of 500 takes 913 us
-// so, 9289 whole; 3000 among 63 of 40 86 us and 298; 64 of 100 tokens 83 and 68, 64 of 512 198 and 210. Not below 2048 tokens,
+// so, 9289 whole; 3000 among 63 of 40 86 us and 298; 64 of 100 tokens 83 and 68, 64 of 512 202 and 203. Not below 2048 tokens,
 // nor where sequences are shorter than a chunk in the mean, since the workspace has a state for each of them. The backward's
 // states are of all segments.
 inline AttnPlan attn_plan(int64_t T, int64_t nseq, int64_t units, bool packed, bool backward) {

@@ -205,8 +205,8 @@ __device__ __forceinline__ unsigned last_up_to(unsigned at, unsigned n, Key key)
 
 // Slots are segments of a.seg tokens; without a split (a.seg 0) slots are sequences. Packed: the segments of sequence s begin at
 // slot cu[s] / seg + s. Cuts are where a segment ends and its sequence goes on: those of sequence s begin at cut cu[s] / seg (s
-// (per_seq - 1) if not packed), so that slot i of sequence s lies between cuts i - s - 1 and i - s. With `cut`, the segment before
-// a cut is asked for. Boundaries are held inside the row whatever cu_seqlens has.
+// (per_seq - 1) if not packed), so that cut i of sequence s lies behind slot i + s. With `cut`, the segment before a cut is asked
+// for. Boundaries are held inside the row whatever cu_seqlens has.
 __device__ __forceinline__ Span span_of(const AttnArgs &a, unsigned slot, bool cut = false) {
     Span p;
     const unsigned seg = (unsigned)a.seg;
@@ -233,6 +233,7 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, unsigned slot, bool c
         end = uniform(a.cu[s + 1]);
         end = end < from ? from : end > T ? T : end;
     }
+    if (cut) p.slot += p.seq;
     p.t0 = from;
     p.len = end - from;
     const int64_t lo = (int64_t)piece * seg;
@@ -346,10 +347,6 @@ __global__ __launch_bounds__(NW * 64, DA > 128 ? 1 : NW / 2) void sweep_kernel(A
     const unsigned slice = unit - member * a.by_slices.d, kh = outer - slot * Hk, head = kh * a.group + member;
     const Span sp = span_of(a, slot, !OUT && r.cuts);
     if (!sp.some) return;
-    // the cut before a segment that a state enters over
-    const bool over = OUT && r.cuts && !sp.first();
-    const unsigned before = (unsigned)(sp.slot - sp.seq - 1);
-    if (over && before >= a.cuts) return;  // (boundaries that are none)
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
     const int wave = uniform(tid >> 6);
@@ -418,10 +415,12 @@ __global__ __launch_bounds__(NW * 64, DA > 128 ? 1 : NW / 2) void sweep_kernel(A
     for (int t = 0; t < TA; ++t)
 #pragma unroll
         for (int n = 0; n < NT; ++n) h[t][n] = zero4();
-    const float *s_in = over ? r.s_cuts : r.s_in;
+    // (of a sequence that is cut the first one too: its last one may write over the state that the sequence begins with)
+    const bool of_cut = OUT && r.cuts && !(sp.first() && sp.last());
+    const float *s_in = of_cut ? r.s_cuts : r.s_in;
     if (OUT && s_in && active) {
-        const float *p = s_in + ((int64_t)(over ? (int)before : r.in_slots ? sp.slot : sp.seq) * Hv + head) * da * db;
-        if (over || r.in_turned) {
+        const float *p = s_in + ((int64_t)(of_cut || r.in_slots ? sp.slot : sp.seq) * Hv + head) * da * db;
+        if (of_cut || r.in_turned) {
 #pragma unroll
             for (int t = 0; t < TA; ++t)
 #pragma unroll
@@ -730,11 +729,10 @@ __device__ __forceinline__ double sum_all(double v, double *held) {
     return held[0] + held[1] + held[2] + held[3];
 }
 
-// Four elements of one head's state a thread: each segment's own state is replaced by the one that enters it, or, with `cuts`
-// (packed, the first one of a sequence names the workgroup), that of the segment before each cut by the one that goes over it.
-// States are [rows][cols] here, init and last the same or, turned, [cols][rows]. With `ends` (backwards, behind the forward's
-// states), each workgroup leaves its part of <the adjoint that enters segment i from behind, the state there>, which enters
-// segment i + 1.
+// Four elements of one head's state a thread: each segment's own state is replaced by the one that enters it. States are
+// [rows][cols] here, init and last the same or, turned, [cols][rows]. With `ends` (backwards, behind the forward's states), each
+// workgroup leaves its part of <the adjoint that enters segment i from behind, the state there>, which enters segment i + 1. With
+// `cuts`, packed sequences of one segment are left out (a sequence's first cut names the workgroup).
 struct Join {
     float *states;
     const float *decays, *init;
@@ -752,14 +750,14 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Join j) {
     if (which >= (j.cuts && a.cu ? a.cuts : a.nseq)) return;
     const int64_t e = block * 1024 + threadIdx.x * 4;
     unsigned seq = which;
-    int n = (int)a.per_seq - (j.cuts ? 1 : 0), first = (int)which * n;
+    int first = (int)(which * a.per_seq), n = (int)a.per_seq;
     if (j.cuts && a.cu) {
         const Span sp = span_of(a, which, true);
         if (!sp.some || !sp.first()) return;
         seq = (unsigned)sp.seq;
-        first = (int)which;
-        n = (sp.len - 1) / (int)a.seg;
-        if ((int64_t)first + n > a.cuts) return;  // boundaries that are none
+        first = sp.slot;
+        n = (sp.len - 1) / (int)a.seg + 1;
+        if ((int64_t)first + n > a.slots) return;  // boundaries that are none
     } else if (a.cu) {
         const int from = a.cu[seq], len = a.cu[seq + 1] - from;
         first = (int)(a.by_seg((unsigned)from) + seq);
@@ -783,7 +781,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Join j) {
         for (int p = 0; p < kAhead; ++p) {
             s[p] = x[p] = zero4();
             d[p] = 0.f;
-            if (i + p + 1 < n || (i + p < n && (j.last || j.cuts))) {
+            if (i + p + 1 < n || (i + p < n && j.last)) {
                 s[p] = *reinterpret_cast<const floatx4 *>(j.states + (slot(i + p) * a.Hv + head) * elems + e);
                 d[p] = j.decays[slot(i + p) * a.Hv + head];
             }
@@ -802,9 +800,8 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Join j) {
                     v = sum_all(v, held);
                     if (threadIdx.x == 0) j.ends[(slot(i + p) * a.Hv + head) * blocks + block] = v;
                 }
-                const floatx4 next = d[p] * h + s[p];
-                *reinterpret_cast<floatx4 *>(j.states + (slot(i + p) * a.Hv + head) * elems + e) = j.cuts ? next : h;
-                h = next;
+                *reinterpret_cast<floatx4 *>(j.states + (slot(i + p) * a.Hv + head) * elems + e) = h;
+                h = d[p] * h + s[p];
             }
     }
     if (j.last) {

@@ -127,3 +127,16 @@ def test_other_boundaries_in_one_graph(gdr, dtype):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(held, both())), i
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("lens,H,packed", [([2000] * 3, 4, False), ([40] * 30 + [3000] + [40] * 33, 16, True), ([0, 700, 1, 0, 2500, 900], 2, True), ([60000], 1, False)])
+def test_states_in_place(gdr, lens, H, packed, dtype):
+    """The final states may replace the initial ones, of sequences that are cut too: all reads of them come before."""
+    say("states in place %d sequences of %d tokens %s" % (len(lens), sum(lens), dtype))
+    q, k, v, la, h, cu = cuda(attn_case(lens, H, H, 64, 64, dtype, 995 + len(lens), packed))
+    out, hT = gdr.linear_attn_fwd(q, k, v, la, h, cu)
+    for _ in range(5):
+        state = h.clone()
+        again, same = gdr.linear_attn_fwd(q, k, v, la, state, cu, hT=state)
+        assert same is state and torch.equal(again, out) and torch.equal(state, hT)
