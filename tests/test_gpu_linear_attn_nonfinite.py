@@ -10,7 +10,7 @@ import pytest
 import torch
 
 from oracle import linear_attn as O
-from tests._attn import TOL, attn_case, decay_bound, upstream
+from tests._attn import attn_case, decay_bound, upstream
 from tests._layers import BF16, FP32, cuda, say
 
 pytestmark = pytest.mark.gpu
